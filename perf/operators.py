@@ -1,10 +1,10 @@
-"""What is measured of the serving operators around mixture-of-depths attention.
+"""What is measured of the operators for ragged batches around mixture-of-depths attention.
 
-Four operators, each in a plain form (elementary torch operations in 32 bits) and as the
-framework's own call:
+Each in a plain form (elementary torch operations in 32 bits) and as the framework's own call:
 
   packed   attention over whole prompts of different lengths that lie one behind the other,
            each query seeing its own sequence's keys up to itself and its own depth entries
+  train    the same forward and then its backward: all gradients for a given upstream one
   tree     attention of N drafted tokens per sequence, a tree given by parents, over a cache
            whose sequences have different lengths (N = 1: one new token per sequence)
   score    the attention weight that the newest N queries give to each cached key, summed
@@ -32,24 +32,24 @@ def listed():
         # a handful of short prompts that arrive together: latency
         dict(name="packed-short", op="packed", nseq=5, total=411, pad=13, Hq=16, Hkv=4, d=128,
              L=24, mix=1),
-        # an ordinary prefill batch at the 1.5B layer's shape
-        dict(name="packed-16k", op="packed", nseq=24, total=16384, pad=0, Hq=16, Hkv=4, d=128,
-             L=24, mix=2),
         # the longest prefill: six documents in 64K tokens
         dict(name="packed-64k", op="packed", nseq=6, total=65536, pad=0, Hq=16, Hkv=4, d=128,
              L=32, mix=3),
         # odd everything: groups of three heads, head size 64, one-token sequences
         dict(name="packed-odd-d64", op="packed", nseq=37, total=5003, pad=6, Hq=6, Hkv=2, d=64,
              L=7, mix=4),
+        # a training step's attention: two dozen documents in 16K tokens, the 1.5B layer's shape
+        dict(name="train-16k", op="train", nseq=24, total=16384, pad=0, Hq=16, Hkv=4, d=128,
+             L=24, mix=2),
+        # short odd documents, with rows behind the last one
+        dict(name="train-odd-d64", op="train", nseq=11, total=2003, pad=9, Hq=6, Hkv=2, d=64,
+             L=5, mix=13),
         # one new token per sequence over short caches: latency
         dict(name="tree-one-token", op="tree", B=4, N=1, S=1000, Hq=16, Hkv=4, d=128, L=24,
              mix=5),
         # one new token per sequence, a full batch of ragged caches
         dict(name="tree-batch32", op="tree", B=32, N=1, S=32768, Hq=16, Hkv=4, d=128, L=48,
              mix=6),
-        # a drafted tree of 24 tokens over eight ragged caches
-        dict(name="tree-24-drafts", op="tree", B=8, N=24, S=16384, Hq=16, Hkv=4, d=128, L=24,
-             mix=7),
         # a wide tree over the longest caches, head layout of the deep stack
         dict(name="tree-61-drafts-64k", op="tree", B=2, N=61, S=65536, Hq=32, Hkv=8, d=128, L=32,
              mix=8),
@@ -71,13 +71,13 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["packed", "tree", "score", "evict"])
+    op = rng.choice(["packed", "train", "tree", "score", "evict"])
     d = rng.choice([64, 128])
     Hkv = rng.choice([1, 2, 4, 8])
     Hq = Hkv * rng.choice([1, 2, 3, 4, 8])
     c = dict(op=op, Hkv=Hkv, d=d, mix=rng.randrange(1 << 20))
-    if op == "packed":
-        total = _log(rng, 200, 30000)
+    if op in ("packed", "train"):
+        total = _log(rng, 200, 30000 if op == "packed" else 8000)
         c.update(Hq=Hq, total=total, nseq=_log(rng, 1, min(200, total // 4)),
                  pad=rng.randrange(20), L=rng.choice([0, 1, 3, 8, 17, 24, 32]))
     elif op == "tree":
@@ -101,7 +101,7 @@ def draw(rng):
 def _lengths(c):
     """Sequence lengths of a case: a spread of a few long and many short ones."""
     r = random.Random(c["mix"])
-    if c["op"] == "packed":
+    if c["op"] in ("packed", "train"):
         n, total = c["nseq"], c["total"]
         w = [math.exp(r.gauss(0.0, 1.0)) for _ in range(n)]
         lens = [int(total * x / sum(w)) for x in w]
@@ -140,7 +140,7 @@ def prepare(case, seed):
     s = dict(case=c, lens=lens, scale=1.0 / math.sqrt(c["d"]))
     Hkv, d = c["Hkv"], c["d"]
     zeros = lambda *shape, dtype: torch.zeros(*shape, device="cuda", dtype=dtype)  # noqa: E731
-    if c["op"] == "packed":
+    if c["op"] in ("packed", "train"):
         n, L, Hq = c["total"] + c["pad"], c["L"], c["Hq"]
         s.update(q=_randn(g, Hq, n, d), k=_randn(g, Hkv, n, d), v=_randn(g, Hkv, n, d),
                  kd=_randn(g, Hkv, n, L, d) if L else None,
@@ -151,6 +151,11 @@ def prepare(case, seed):
         s["cu"] = torch.tensor(ends, device="cuda", dtype=torch.int32)
         # rows behind the last sequence are left as they were: zeros here
         s["out"], s["lse"] = zeros(Hq, n, d, dtype=BF), zeros(Hq, n, dtype=torch.float32)
+        if c["op"] == "train":
+            s["dout"] = _randn(g, Hq, n, d)
+            s["grads"] = {"d" + x: zeros(*s[x].shape, dtype=BF) for x in ("q", "k", "v")}
+            if L:
+                s["grads"].update({"d" + x: zeros(*s[x].shape, dtype=BF) for x in ("kd", "vd")})
         return s
     B, S = c["B"], c["S"]
     s["lengths"] = torch.tensor(lens, device="cuda", dtype=torch.int32)
@@ -191,10 +196,13 @@ def run(state):
     op = state["case"]["op"]
     if own:
         import depth_aware_attention_b200 as moda
-        if op == "packed":
-            return moda.forward_packed(state["q"], state["k"], state["v"], state["cu"],
-                                       state["kd"], state["vd"], out=state["out"],
-                                       lse=state["lse"])
+        if op in ("packed", "train"):
+            x = [state[n] for n in ("q", "k", "v", "cu", "kd", "vd")]
+            out, lse = moda.forward_packed(*x, out=state["out"], lse=state["lse"])
+            if op == "packed":
+                return out, lse
+            grads = moda.backward_packed(*x, out, lse, state["dout"], grads=state["grads"])
+            return out, lse, {n: grads[n] for n in state["grads"]}
         if op == "tree":
             return moda.tree_decode(state["q"], state["k"], state["v"], state["kt"], state["vt"],
                                     state["parents"], state["lengths"], state["kd"], state["vd"])
@@ -204,7 +212,7 @@ def run(state):
         return moda.cache_evict(state["k"], state["v"], state["score"], state["lengths"],
                                 state["case"]["keep"], state["case"]["sinks"],
                                 state["case"]["recent"], **state["outs"])
-    return {"packed": _packed, "tree": _tree, "score": _score, "evict": _evict}[op](state)
+    return {"packed": _packed, "train": _train, "tree": _tree, "score": _score, "evict": _evict}[op](state)
 
 
 def _packed(s):
@@ -239,6 +247,49 @@ def _packed(s):
             lse[:, first + a:first + b] = (top + torch.log(total)).reshape(Hq, b - a)
         first += x
     return out, lse
+
+
+def _train(s):
+    c, scale = s["case"], s["scale"]
+    Hq, Hkv, d, L = c["Hq"], c["Hkv"], c["d"], c["L"]
+    G = Hq // Hkv
+    out, lse = _packed(s)
+    dq, dk, dv = (torch.zeros(s[x].shape, device="cuda") for x in ("q", "k", "v"))
+    dkd, dvd = (torch.zeros(s[x].shape, device="cuda", dtype=BF) if L else None
+                for x in ("kd", "vd"))
+    first = 0
+    for x in s["lens"]:
+        for a in range(0, x, 2048):
+            b = min(x, a + 2048)
+            row, key = slice(first + a, first + b), slice(first, first + b)
+            q, do = (s[n][:, row].float().view(Hkv, G, b - a, d) for n in ("q", "dout"))
+            k, v = s["k"][:, key].float(), s["v"][:, key].float()
+            z = torch.einsum("hgtd,hsd->hgts", q, k) * scale
+            t = torch.arange(a, b, device="cuda")
+            z = z.masked_fill(torch.arange(b, device="cuda")[None, :] > t[:, None], -math.inf)
+            top = lse[:, row].view(Hkv, G, b - a, 1)
+            p = torch.exp(z - top)
+            o = torch.einsum("hgts,hsd->hgtd", p, v)
+            if L:
+                kd, vd = s["kd"][:, row].float(), s["vd"][:, row].float()
+                py = torch.exp(torch.einsum("hgtd,htld->hgtl", q, kd) * scale - top)
+                o = o + torch.einsum("hgtl,htld->hgtd", py, vd)
+            whole = (o * do).sum(-1, keepdim=True)
+            ds = p * (torch.einsum("hgtd,hsd->hgts", do, v) - whole) * scale
+            g = torch.einsum("hgts,hsd->hgtd", ds, k)
+            dk[:, key] += torch.einsum("hgts,hgtd->hsd", ds, q)
+            dv[:, key] += torch.einsum("hgts,hgtd->hsd", p, do)
+            if L:
+                dy = py * (torch.einsum("hgtd,htld->hgtl", do, vd) - whole) * scale
+                g = g + torch.einsum("hgtl,htld->hgtd", dy, kd)
+                dkd[:, row] = torch.einsum("hgtl,hgtd->htld", dy, q).to(BF)
+                dvd[:, row] = torch.einsum("hgtl,hgtd->htld", py, do).to(BF)
+            dq[:, row] = g.reshape(Hq, b - a, d)
+        first += x
+    grads = dict(dq=dq.to(BF), dk=dk.to(BF), dv=dv.to(BF))
+    if L:
+        grads.update(dkd=dkd, dvd=dvd)
+    return out, lse, grads
 
 
 def _ancestors(parents):
@@ -317,11 +368,13 @@ def work(case):
     c, lens = case, _lengths(case)
     Hkv, d = c["Hkv"], c["d"]
     tokens = sum(lens)
-    if c["op"] == "packed":
+    if c["op"] in ("packed", "train"):
         Hq, L = c["Hq"], c["L"]
         pairs = sum(x * (x + 1) // 2 for x in lens) + tokens * L
-        return dict(bytes=tokens * (Hq * (4 * d + 4) + Hkv * 4 * d * (1 + L)),
-                    flops=4 * Hq * d * pairs)
+        both = c["op"] == "train"  # dout in, every gradient out; ten more products than four
+        return dict(bytes=tokens * (Hq * (4 * d + 4) + Hkv * 4 * d * (1 + L)
+                                    + (Hq * 4 * d + Hkv * 4 * d * (1 + L) if both else 0)),
+                    flops=(14 if both else 4) * Hq * d * pairs)
     if c["op"] == "tree":
         Hq, L, N, B = c["Hq"], c["L"], c["N"], c["B"]
         pairs = N * tokens + B * N * (L + (N + 1) / 2)
@@ -337,7 +390,7 @@ def work(case):
 # ---------------------------------------------------------------------------- in 64 bits
 def exact(case, seed):
     s = prepare(case, seed)
-    return {"packed": _exact_packed, "tree": _exact_tree, "score": _exact_score,
+    return {"packed": _exact_packed, "train": _exact_train, "tree": _exact_tree, "score": _exact_score,
             "evict": _exact_evict}[case["op"]](s)
 
 
@@ -373,6 +426,34 @@ def _exact_packed(s):
                         values.append(s["vd"][g, t:u].double())
                     out[h, t:u], lse[h, t:u] = _softmax_row_block(logits, values)
     return out, lse
+
+
+def _exact_train(s):
+    c = s["case"]
+    G, L = c["Hq"] // c["Hkv"], c["L"]
+    names = ("q", "k", "v") + (("kd", "vd") if L else ())
+    grads = {"d" + n: torch.zeros(s[n].shape, device="cuda", dtype=torch.float64) for n in names}
+    out = torch.zeros(s["q"].shape, device="cuda", dtype=torch.float64)
+    lse = torch.zeros(s["q"].shape[:2], device="cuda", dtype=torch.float64)
+    ends = s["cu"].tolist()
+    for a, e in zip(ends[:-1], ends[1:]):
+        hide = torch.ones(e - a, e - a, device="cuda").triu(1).bool()
+        for g in range(c["Hkv"] if e > a else 0):
+            leaf = {n: s[n][g, a:e].double().requires_grad_() for n in names[1:]}
+            for h in range(g * G, g * G + G):
+                q = s["q"][h, a:e].double().requires_grad_()
+                logits = [(q @ leaf["k"].T * s["scale"]).masked_fill(hide, -math.inf)]
+                values = [leaf["v"]]
+                if L:
+                    logits.append((leaf["kd"] @ q[..., None])[..., 0] * s["scale"])
+                    values.append(leaf["vd"])
+                o, lse_h = _softmax_row_block(logits, values)
+                (o * s["dout"][h, a:e].double()).sum().backward()
+                out[h, a:e], lse[h, a:e] = o.detach(), lse_h.detach()
+                grads["dq"][h, a:e] = q.grad
+            for n, x in leaf.items():
+                grads["d" + n][g, a:e] = x.grad
+    return out, lse, grads
 
 
 def _exact_tree(s):
