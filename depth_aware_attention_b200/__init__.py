@@ -31,7 +31,7 @@ BACKWARD_LAUNCHES = 3
 # Every symbol include/moda.h declares (checked by the ABI tests).
 EXPORTED = ("moda_forward", "moda_forward_depth_path", "moda_depth_attention_forward",
             "moda_depth_attention_backward", "moda_decode", "moda_decode_workspace_size",
-            "moda_depth_kv_write",
+            "moda_depth_kv_write", "moda_forward_packed", "moda_backward_packed",
             "moda_backward", "moda_backward_workspace_size",
             "moda_backward_stages", "moda_backward_noalloc", "moda_check_device_errors",
             "moda_test_set_device_fault", "moda_test_exp2_fma", "moda_status_string",
@@ -73,6 +73,10 @@ def _load():
     lib.moda_backward_stages.restype = I
     lib.moda_backward_noalloc.argtypes = [P] * 13 + [I] * 6 + [F, I, P]
     lib.moda_backward_noalloc.restype = I
+    lib.moda_forward_packed.argtypes = [P] * 8 + [I] * 6 + [F, I, P]
+    lib.moda_forward_packed.restype = I
+    lib.moda_backward_packed.argtypes = [P] * 15 + [S] + [I] * 6 + [F, I, P]
+    lib.moda_backward_packed.restype = I
     lib.moda_test_set_device_fault.argtypes = [I, ctypes.c_uint64]
     lib.moda_test_set_device_fault.restype = I
     lib.moda_test_exp2_fma.argtypes = [P, P, I, P]
@@ -163,6 +167,22 @@ def moda_backward_stages(q, k, v, kd, vd, out, lse, dout, dq, dk, dv, dkd, dvd, 
     return lib.moda_backward_stages(q, k, v, kd, vd, out, lse, dout, dq, dk, dv, dkd, dvd,
                                     workspace, workspace_bytes, B, Hq, Hkv, T, L, d,
                                     float(scale), int(causal), int(stages), stream)
+
+
+def moda_forward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, Hq, Hkv, N, nseq, L, d, scale,
+                        causal, stream):
+    """Direct call of moda_forward_packed with raw pointers (ints) and a stream handle."""
+    return lib.moda_forward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, Hq, Hkv, N, nseq, L,
+                                   d, float(scale), int(causal), stream)
+
+
+def moda_backward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, dout, dq, dk, dv, dkd, dvd,
+                         workspace, workspace_bytes, Hq, Hkv, N, nseq, L, d, scale, causal,
+                         stream):
+    """Direct call of moda_backward_packed with raw pointers (ints) and a stream handle."""
+    return lib.moda_backward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, dout, dq, dk, dv,
+                                    dkd, dvd, workspace, workspace_bytes, Hq, Hkv, N, nseq, L,
+                                    d, float(scale), int(causal), stream)
 
 
 def moda_backward_workspace_size(B, Hq, Hkv, T, L, d):
@@ -467,3 +487,110 @@ def depth_kv_write(x, w, kd, vd, slot):
     st = lib.moda_depth_kv_write(_ptr(x), _ptr(w), _ptr(kd), _ptr(vd), B, T, hidden, Hkv, d,
                                  L, int(slot), _stream_handle(x.device))
     _check(st, "moda_depth_kv_write")
+
+
+# ---------------------------------------------------------------- ragged batches
+def _checked(device, specs, workspace=None):
+    """_validate for a list of (name, tensor, shape, dtype), written for the calls whose
+    kernels take a few microseconds: one pass of cheap comparisons, and _validate (which
+    says what is wrong) only when one of them fails."""
+    ok = device.type == "cuda" and (workspace is None or (workspace.is_contiguous()
+                                                          and workspace.device == device))
+    for _, t, shape, dtype in specs:
+        ok = (ok and t is not None and t.shape == shape and t.dtype is dtype
+              and t.is_contiguous() and t.device == device)
+    if not ok:
+        _validate(device, {n: (t, shape, dtype) for n, t, shape, dtype in specs}, workspace)
+
+
+def _call(fn, name, device, *args):
+    """Calls the C entry point `fn` with the current stream of `device`, which is made the
+    current device for the call when it is not."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != MODA_OK:
+        raise ModaError(st, name, _msg(st))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _packed_dims(q, k, kd, cu_seqlens):
+    _ndim("q", q, 3)
+    _ndim("k", k, 3)
+    _ndim("cu_seqlens", cu_seqlens, 1)
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold nseq + 1 >= 2 entries")
+    if kd is not None:
+        _ndim("kd", kd, 4)
+    Hq, N, d = q.shape
+    return Hq, k.shape[0], N, cu_seqlens.shape[0] - 1, 0 if kd is None else kd.shape[2], d
+
+
+def forward_packed(q, k, v, cu_seqlens, kd=None, vd=None, scale=None, causal=True, out=None,
+                   lse=None):
+    """MoDA forward over a packed batch on the current CUDA stream.  Returns (out, lse).
+
+    Sequences of different lengths lie one behind the other: q [Hq,N,d], k/v [Hkv,N,d],
+    kd/vd [Hkv,N,L,d] (or None for L = 0), cu_seqlens int32 [nseq+1] on the device, sequence
+    s in rows [cu_seqlens[s], cu_seqlens[s+1]).  Rows outside all sequences are not written
+    (in an `out` and `lse` that the call allocates they hold whatever the memory held).
+    """
+    import torch
+    Hq, Hkv, N, nseq, L, d = _packed_dims(q, k, kd, cu_seqlens)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((Hq, N), device=q.device, dtype=torch.float32)
+    bf = torch.bfloat16
+    spec = [("q", q, (Hq, N, d), bf), ("k", k, (Hkv, N, d), bf), ("v", v, (Hkv, N, d), bf),
+            ("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32), ("out", out, (Hq, N, d), bf),
+            ("lse", lse, (Hq, N), torch.float32)]
+    if L:
+        spec += [("kd", kd, (Hkv, N, L, d), bf), ("vd", vd, (Hkv, N, L, d), bf)]
+    _checked(q.device, spec)
+    _call(lib.moda_forward_packed, "moda_forward_packed", q.device, _at(q), _at(k), _at(v),
+          _at(kd) if L else None, _at(vd) if L else None, _at(cu_seqlens), _at(out), _at(lse), Hq,
+          Hkv, N, nseq, L, d, scale, 1 if causal else 0)
+    return out, lse
+
+
+def backward_packed(q, k, v, cu_seqlens, kd, vd, out, lse, dout, scale=None, causal=True,
+                    workspace=None, grads=None):
+    """MoDA backward over a packed batch on the current CUDA stream.  Returns dict(dq, dk, dv,
+    dkd, dvd); ``out``/``lse`` are forward_packed's, ``workspace``/``grads`` as for backward().
+    The gradients' rows outside all sequences are not written."""
+    import torch
+    Hq, Hkv, N, nseq, L, d = _packed_dims(q, k, kd, cu_seqlens)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = torch.empty(lib.moda_backward_workspace_size(1, Hq, Hkv, N, L, d),
+                                device=q.device, dtype=torch.uint8)
+    g = dict(grads or {})
+    for name, like in (("dq", q), ("dk", k), ("dv", v), ("dkd", kd), ("dvd", vd)):
+        if not L and name in ("dkd", "dvd"):
+            g[name] = None
+        elif g.get(name) is None:
+            g[name] = torch.empty_like(like)
+    bf, qs, kv, ds = torch.bfloat16, (Hq, N, d), (Hkv, N, d), (Hkv, N, L, d)
+    spec = [("q", q, qs, bf), ("k", k, kv, bf), ("v", v, kv, bf),
+            ("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32), ("out", out, qs, bf),
+            ("lse", lse, (Hq, N), torch.float32), ("dout", dout, qs, bf), ("dq", g["dq"], qs, bf),
+            ("dk", g["dk"], kv, bf), ("dv", g["dv"], kv, bf)]
+    if L:
+        spec += [("kd", kd, ds, bf), ("vd", vd, ds, bf), ("dkd", g["dkd"], ds, bf),
+                 ("dvd", g["dvd"], ds, bf)]
+    _checked(q.device, spec, workspace)
+    _call(lib.moda_backward_packed, "moda_backward_packed", q.device, _at(q), _at(k), _at(v),
+          _at(kd) if L else None, _at(vd) if L else None, _at(cu_seqlens), _at(out), _at(lse),
+          _at(dout), _at(g["dq"]), _at(g["dk"]), _at(g["dv"]), _at(g["dkd"]), _at(g["dvd"]),
+          _at(workspace), _nbytes(workspace), Hq, Hkv, N, nseq, L, d, scale, 1 if causal else 0)
+    return g

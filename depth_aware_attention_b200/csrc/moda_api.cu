@@ -15,6 +15,7 @@
 #include "../../include/moda.h"
 #include "moda_internal.h"
 #include "sm100.cuh"
+#include "moda_packed.cuh"
 
 namespace {
 
@@ -48,6 +49,20 @@ moda_status_t check_sizes(int B, int Hq, int Hkv, int T, int L, int d) {
   // index arithmetic in the kernels uses 32-bit tile/row counts and 64-bit offsets
   const long long rows = 1LL * B * Hq * T;
   if (rows > (1LL << 31) || 1LL * B * Hkv > 65535 || T > (1 << 30) || L > 65535)
+    return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");
+  return MODA_OK;
+}
+
+// The sequence bounds of a packed call (cu null: not a packed call, nothing to check).  Their
+// values are known on the device alone; the kernels check them.
+moda_status_t check_packed(const int* cu, int nseq, int Hq, int Hkv, int N, float scale) {
+  if (cu == nullptr) return MODA_OK;
+  if (reinterpret_cast<uintptr_t>(cu) & 3u)
+    return fail(MODA_ERR_INVALID_ARGUMENT, "cu_seqlens must be 4-byte aligned");
+  if (nseq < 1) return fail(MODA_ERR_INVALID_ARGUMENT, "nseq must be at least 1");
+  if (!(scale > 0.f)) return fail(MODA_ERR_INVALID_ARGUMENT, "scale must be positive");
+  const long long unit = 2 * (128 / (Hq / Hkv));  // the smaller piece of the two passes
+  if (Hkv * moda::packed_pieces_bound(N, nseq, unit < 128 ? unit : 128) > 0x7fffffffll)
     return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");
   return MODA_OK;
 }
@@ -140,11 +155,14 @@ static moda_status_t forward_entry(const void* q, const void* k, const void* v,
                                    const void* kd, const void* vd, void* out, float* lse,
                                    int B, int Hq, int Hkv, int T, int L, int d, float scale,
                                    int causal, int depth_path, int depth_only,
-                                   moda_stream_t stream) {
+                                   moda_stream_t stream, const int* cu = nullptr,
+                                   int nseq = 0) {
   g_msg[0] = 0;
   moda_status_t s = injected_at_validate();
   if (s != MODA_OK) return s;
   s = check_sizes(B, Hq, Hkv, T, L, d);
+  if (s != MODA_OK) return s;
+  s = check_packed(cu, nseq, Hq, Hkv, T, scale);
   if (s != MODA_OK) return s;
   if (depth_only) {
     if (L < 1) return fail(MODA_ERR_INVALID_ARGUMENT, "depth-only attention needs L >= 1");
@@ -171,8 +189,13 @@ static moda_status_t forward_entry(const void* q, const void* k, const void* v,
       return fail(MODA_ERR_INVALID_ARGUMENT, "out/lse must not overlap an input");
   if (overlaps(out, nq, lse, nl))
     return fail(MODA_ERR_INVALID_ARGUMENT, "out and lse must not overlap");
+  if (cu && (overlaps(out, nq, cu, 4 * (size_t(nseq) + 1)) ||
+             overlaps(lse, nl, cu, 4 * (size_t(nseq) + 1))))
+    return fail(MODA_ERR_INVALID_ARGUMENT, "out/lse must not overlap an input");
   moda::Problem p{B, Hq, Hkv, T, L, d, Hq / Hkv, causal ? 1 : 0, scale};
   p.depth_only = depth_only ? 1 : 0;
+  p.cu = cu;
+  p.nseq = nseq;
   if (depth_path == moda::kDepthPathDense && !moda::dense_depth_supported(p))
     return fail(MODA_ERR_UNSUPPORTED, "dense depth blocks need Hq/Hkv to divide 128");
   s = injected_at_launch();
@@ -214,6 +237,18 @@ moda_status_t moda_forward_depth_path(const void* q, const void* k, const void* 
                                       moda_stream_t stream) {
   return forward_entry(q, k, v, kd, vd, out, lse, B, Hq, Hkv, T, L, d, scale, causal,
                        depth_path, 0, stream);
+}
+
+moda_status_t moda_forward_packed(const void* q, const void* k, const void* v, const void* kd,
+                                  const void* vd, const int32_t* cu_seqlens, void* out,
+                                  float* lse, int Hq, int Hkv, int N, int nseq, int L, int d,
+                                  float scale, int causal, moda_stream_t stream) {
+  if (!cu_seqlens) {
+    g_msg[0] = 0;
+    return fail(MODA_ERR_INVALID_ARGUMENT, "cu_seqlens must be non-NULL");
+  }
+  return forward_entry(q, k, v, kd, vd, out, lse, 1, Hq, Hkv, N, L, d, scale, causal,
+                       moda::kDepthPathAuto, 0, stream, cu_seqlens, nseq);
 }
 
 size_t moda_decode_workspace_size(int B, int Hq, int Hkv, int S, int L, int d) {
@@ -337,11 +372,14 @@ moda_status_t backward_entry(const void* q, const void* k, const void* v, const 
                              void* dvd, void* workspace, size_t workspace_bytes, int B,
                              int Hq, int Hkv, int T, int L, int d, float scale, int causal,
                              unsigned stages, int depth_only, moda_stream_t stream,
-                             bool validate_only = false) {
+                             bool validate_only = false, const int* cu = nullptr,
+                             int nseq = 0) {
   g_msg[0] = 0;
   moda_status_t s = injected_at_validate();
   if (s != MODA_OK) return s;
   s = check_sizes(B, Hq, Hkv, T, L, d);
+  if (s != MODA_OK) return s;
+  s = check_packed(cu, nseq, Hq, Hkv, T, scale);
   if (s != MODA_OK) return s;
   if (depth_only) {
     if (L < 1) return fail(MODA_ERR_INVALID_ARGUMENT, "depth-only attention needs L >= 1");
@@ -365,6 +403,8 @@ moda_status_t backward_entry(const void* q, const void* k, const void* v, const 
     return fail(MODA_ERR_INVALID_ARGUMENT, "scale must be finite");
   moda::Problem p{B, Hq, Hkv, T, L, d, Hq / Hkv, causal ? 1 : 0, scale};
   p.depth_only = depth_only ? 1 : 0;
+  p.cu = cu;
+  p.nseq = nseq;
   if (validate_only) {
     // the checks of the gradient buffers against the inputs and each other
     const size_t nq = size_t(B) * Hq * T * d * 2, nk = size_t(B) * Hkv * T * d * 2;
@@ -388,12 +428,12 @@ moda_status_t backward_entry(const void* q, const void* k, const void* v, const 
     return fail(MODA_ERR_INVALID_ARGUMENT, "workspace is smaller than moda_backward_workspace_size()");
   const size_t nq = size_t(B) * Hq * T * d * 2, nk = size_t(B) * Hkv * T * d * 2;
   const size_t nd = nk * size_t(L), nl = size_t(B) * Hq * T * 4;  // (k, v unused: NULL)
-  const void* ins[8] = {q, k, v, kd, vd, out, lse, dout};
-  const size_t insz[8] = {nq, nk, nk, nd, nd, nq, nl, nq};
+  const void* ins[9] = {q, k, v, kd, vd, out, lse, dout, cu};
+  const size_t insz[9] = {nq, nk, nk, nd, nd, nq, nl, nq, 4 * (size_t(nseq) + 1)};
   void* outs[6] = {dq, dk, dv, dkd, dvd, workspace};
   const size_t outsz[6] = {nq, nk, nk, nd, nd, need};
   for (int o = 0; o < 6; ++o) {
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 9; ++i)
       if (overlaps(outs[o], outsz[o], ins[i], insz[i]))
         return fail(MODA_ERR_INVALID_ARGUMENT, "gradient/workspace buffers must not overlap an input");
     for (int o2 = o + 1; o2 < 6; ++o2)
@@ -446,6 +486,22 @@ moda_status_t moda_backward_stages(const void* q, const void* k, const void* v,
   return backward_entry(q, k, v, kd, vd, out, lse, dout, dq, dk, dv, dkd, dvd, workspace,
                         workspace_bytes, B, Hq, Hkv, T, L, d, scale, causal, stages, 0,
                         stream);
+}
+
+moda_status_t moda_backward_packed(const void* q, const void* k, const void* v, const void* kd,
+                                   const void* vd, const int32_t* cu_seqlens, const void* out,
+                                   const float* lse, const void* dout, void* dq, void* dk,
+                                   void* dv, void* dkd, void* dvd, void* workspace,
+                                   size_t workspace_bytes, int Hq, int Hkv, int N, int nseq,
+                                   int L, int d, float scale, int causal,
+                                   moda_stream_t stream) {
+  if (!cu_seqlens) {
+    g_msg[0] = 0;
+    return fail(MODA_ERR_INVALID_ARGUMENT, "cu_seqlens must be non-NULL");
+  }
+  return backward_entry(q, k, v, kd, vd, out, lse, dout, dq, dk, dv, dkd, dvd, workspace,
+                        workspace_bytes, 1, Hq, Hkv, N, L, d, scale, causal, moda::kStagesAll,
+                        0, stream, false, cu_seqlens, nseq);
 }
 
 moda_status_t moda_depth_attention_backward(const void* q, const void* kd, const void* vd,

@@ -24,6 +24,15 @@
 //     shared memory and added by the TMA unit (bulk tensor reduce-add), for d = 128 (the
 //     half-tile variant, 2b) straight from registers with global reductions.
 //  3. moda_dq_convert_kernel: dq (bf16) from the fp32 accumulator.
+//
+// Packed batches (template flag kPacked): sequences of different lengths lie one behind the
+// other in one token axis.  The depth kernel and the conversion skip the tokens outside all
+// sequences; a CTA of the sequence kernels owns 128 keys of ONE sequence (found by
+// packed_find) and walks the query tiles that hold that sequence's rows.  The tiles keep
+// their places on the whole token axis (the row-term records are laid out by them), so the
+// first and the last tile of a walk, and the key block at a sequence's end, may hold rows of
+// a neighbour: one more warp zeroes those rows of Q, dO, K and V before the tensor cores
+// read them, and their row terms are set to weight zero.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,6 +42,7 @@
 
 #include "moda_internal.h"
 #include "sm100.cuh"
+#include "moda_packed.cuh"
 
 namespace moda {
 
@@ -80,7 +90,15 @@ struct BwdDepthArgs {
   int head0, Gfull, acc_mode;
   float *dkd_acc, *dvd_acc;  // [B][Hkv][T][L][D] fp32 (acc_mode != 0)
   float scale, scale_log2;
+  const int* cu;  // packed: [nseq + 1] first rows of the sequences
+  int nseq;
 };
+
+// Token rows of a packed batch that belong to a sequence: [lo, hi).
+__device__ __forceinline__ void packed_rows(const int* cu, int nseq, int N, int& lo, int& hi) {
+  lo = max(0, __ldg(cu));
+  hi = min(N, __ldg(cu + nseq));
+}
 
 // One token slot = D/8 consecutive threads (one 16-byte column chunk each); a CTA works
 // on kDepthThreads/(D/8) consecutive tokens of the flattened [B*Hkv][T] token list at a
@@ -112,7 +130,7 @@ __host__ __device__ constexpr int bf_head(int lane, int i) {
 
 // kRT: also write the tiled row-term records (a.rt, the d = 128 sequence kernel's input);
 // the instantiation without them is the one depth-only attention and d = 64 run.
-template <int D, int GM, bool kRT>
+template <int D, int GM, bool kRT, bool kPacked>
 // (GM <= 4: at most 168 registers, three CTAs per SM; measured faster than 188 registers
 // and two CTAs)
 __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
@@ -146,13 +164,17 @@ __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
   const uint32_t stage_slot =
       ring + uint32_t(kDepthStageBytes) + uint32_t(slot) * uint32_t(L) * uint32_t(GM * 8);
 
+  int row_lo = 0, row_hi = 0;
+  if constexpr (kPacked) packed_rows(a.cu, a.nseq, a.T, row_lo, row_hi);
+
   for (long long base = (long long)blockIdx.x * TPB; base < a.ntok;
        base += (long long)gridDim.x * TPB) {
     const long long tk = base + slot;
-    const bool valid = tk < a.ntok;
-    const long long tkc = valid ? tk : a.ntok - 1;
+    const bool inside = tk < a.ntok;
+    const long long tkc = inside ? tk : a.ntok - 1;
     const long long bg = tkc / a.T;
     const int t = int(tkc - bg * a.T);
+    const bool valid = inside && (!kPacked || (t >= row_lo && t < row_hi));
     const int qt = kRT ? t / a.TQ : 0, tq = t - qt * a.TQ;
     float* const rt_tile = kRT ? a.rt + ((bg * a.nqt + qt) << 8) : nullptr;
     const int r0 = tq * a.Gfull + a.head0;  // tile row of this chunk's head 0
@@ -659,6 +681,7 @@ struct SeqBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t do_full[2], do_empty[2];
   uint64_t s_full, dp_full, pds_full, dq_full, dq_free, kv_done;
+  uint64_t kv_clean, q_clean[2], do_clean[2];  // packed: neighbours' rows zeroed
   uint32_t tmem_base;
   int abort;
 };
@@ -670,10 +693,54 @@ struct SeqArgs {
   const float* rt;          // d = 128 kernel: tiled row terms (BwdDepthArgs::rt)
   int Hkv, T, G, TQ, nqt, BG, causal;
   float scale, scale_log2;
+  const int* cu;  // packed: [nseq + 1] first rows of the sequences (T is the row count N)
+  int nseq;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kSeqThreads, 1)
+// What one CTA of the sequence kernels owns: keys [key0, min(key0 + 128, row1)) of the
+// sequence in rows [row0, row1), and the query tiles [first_qt, first_qt + ntiles) that hold
+// rows which see them.
+struct SeqSpan {
+  int key0, row0, row1, first_qt, ntiles;
+  bool head, tail;  // the first / last tile holds rows of a neighbour
+};
+template <bool kPacked>
+__device__ __forceinline__ bool seq_span(const SeqArgs& a, SeqSpan& w) {
+  const int kb = blockIdx.x / a.BG;  // key blocks nearest the start see the most tiles
+  if constexpr (kPacked) {
+    const PackedPiece pc = packed_find(a.cu, a.nseq, a.T, 128, kb);
+    if (!pc.found) return false;  // the grid is sized by an upper bound
+    w.row0 = pc.first;
+    w.row1 = pc.first + pc.len;
+    w.key0 = pc.first + 128 * (pc.n - 1 - pc.p);
+    w.first_qt = (a.causal ? w.key0 : w.row0) / a.TQ;
+    w.ntiles = (w.row1 - 1) / a.TQ - w.first_qt + 1;
+    w.head = w.first_qt * a.TQ < w.row0;
+    w.tail = (w.first_qt + w.ntiles) * a.TQ > w.row1;
+  } else {
+    w.row0 = 0;
+    w.row1 = a.T;
+    w.key0 = kb * 128;
+    w.first_qt = a.causal ? w.key0 / a.TQ : 0;
+    w.ntiles = a.nqt - w.first_qt;
+    w.head = w.tail = false;
+  }
+  return true;
+}
+// Whether tile i of the walk holds rows of a neighbour.
+__device__ __forceinline__ bool mixed_tile(const SeqSpan& w, int i) {
+  return (w.head && i == 0) || (w.tail && i == w.ntiles - 1);
+}
+// Rows [r0, r1) of tile i belong to the sequence; the others are zeroed in `tile`.
+__device__ __forceinline__ void own_tile_rows(const SeqArgs& a, const SeqSpan& w, int i, int& r0,
+                                              int& r1) {
+  const int t0 = (w.first_qt + i) * a.TQ;
+  r0 = max(0, w.row0 - t0) * a.G;
+  r1 = min(a.TQ, w.row1 - t0) * a.G;
+}
+
+template <int D, bool kPacked>
+__global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
     moda_bwd_seq_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmDO,
                         const __grid_constant__ CUtensorMap tmK,
@@ -698,19 +765,24 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int bg = blockIdx.x % a.BG;
-  const int kb = blockIdx.x / a.BG;  // key blocks nearest the start see the most tiles
-  const int key0 = kb * 128;
-  const int first_qt = a.causal ? key0 / a.TQ : 0;
-  const int ntiles = a.nqt - first_qt;
+  SeqSpan w;
+  if (!seq_span<kPacked>(a, w)) return;
+  const int key0 = w.key0, row1 = w.row1, first_qt = w.first_qt, ntiles = w.ntiles;
+  const bool kv_mixed = kPacked && key0 + 128 > row1;  // the key block reaches past the end
 
   if (threadIdx.x == 0) {
     mbar_init(bar(bars->kv_full), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars->q_full[i]), 1);
-      mbar_init(bar(bars->q_empty[i]), 1);
+      mbar_init(bar(bars->q_empty[i]), kPacked ? 2 : 1);  // packed: warp 10 has seen it too
       mbar_init(bar(bars->do_full[i]), 1);
-      mbar_init(bar(bars->do_empty[i]), 1);
+      mbar_init(bar(bars->do_empty[i]), kPacked ? 2 : 1);
+      if (kPacked) {
+        mbar_init(bar(bars->q_clean[i]), 1);
+        mbar_init(bar(bars->do_clean[i]), 1);
+      }
     }
+    if (kPacked) mbar_init(bar(bars->kv_clean), 1);
     mbar_init(bar(bars->s_full), 1);
     mbar_init(bar(bars->dp_full), 1);
     mbar_init(bar(bars->pds_full), 128);
@@ -780,10 +852,15 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       constexpr uint32_t idesc_t = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
       constexpr uint32_t idesc_g = make_idesc_bf16(128, D, 0, 1);    // dV, dK (A in TMEM)
       constexpr uint32_t idesc_q = make_idesc_bf16(128, D, 1, 1);    // dQ (A = dS, MN-major)
-      mbar_wait(bar(bars->kv_full), 0, abort_flag);
-      // S^T(i) = K Q(i)^T and dP^T(i) = V dO(i)^T
+      mbar_wait(bar(kv_mixed ? bars->kv_clean : bars->kv_full), 0, abort_flag);
+      // S^T(i) = K Q(i)^T and dP^T(i) = V dO(i)^T.  A tile with a neighbour's rows (packed:
+      // the first and the last of the walk, which have a one-shot barrier each) is waited
+      // for until those are zeroed.
       auto issue_s = [&](int i) {
-        mbar_wait(bar(bars->q_full[i & 1]), (i >> 1) & 1, abort_flag);
+        if (kPacked && mixed_tile(w, i))
+          mbar_wait(bar(bars->q_clean[i == 0 ? 0 : 1]), 0, abort_flag);
+        else
+          mbar_wait(bar(bars->q_full[i & 1]), (i >> 1) & 1, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -794,7 +871,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         tc_commit(bar(bars->s_full));
       };
       auto issue_dp = [&](int i) {
-        mbar_wait(bar(bars->do_full[i & 1]), (i >> 1) & 1, abort_flag);
+        if (kPacked && mixed_tile(w, i))
+          mbar_wait(bar(bars->do_clean[i == 0 ? 0 : 1]), 0, abort_flag);
+        else
+          mbar_wait(bar(bars->do_full[i & 1]), (i >> 1) & 1, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -858,7 +938,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     // stays off the per-tile critical path
     auto load_rowterms = [&](int i, float& lse2v, float& dv_) {
       const int t = (first_qt + i) * a.TQ + tok;
-      const bool valid = i < ntiles && tok < a.TQ && t < a.T;
+      const bool valid = i < ntiles && tok < a.TQ && t < row1 && (!kPacked || t >= w.row0);
       const long long idx = ((long long)bg * a.G + hl) * a.T + (valid ? t : 0);
       lse2v = valid ? -a.lse[idx] * kLog2eBwd : -INFINITY;  // stored negated
       dv_ = valid ? -a.drow[idx] : 0.f;                      // stored negated
@@ -874,7 +954,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       load_rowterms(i + 1, nxt_lse, nxt_d);
       // rows r < r_min hold tokens before this key (causal) -- their weight is zero
       int r_min = 0;
-      if (key >= a.T)
+      if (key >= row1)
         r_min = 1 << 30;
       else if (a.causal)
         r_min = a.G * (key - qt * a.TQ);
@@ -943,7 +1023,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     // epilogue: dV, dK rows of this key
     mbar_wait(bar(bars->kv_done), 0, abort_flag);
     tc_fence_after();
-    const bool kvalid = key < a.T;
+    const bool kvalid = key < row1;
     const long long koff = ((long long)bg * a.T + (kvalid ? key : 0)) * D;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -966,6 +1046,38 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         }
       }
     }
+  } else if (kPacked && warp == 10) {
+    // ------------------------------------------------------------ neighbours' rows
+    const int lane = threadIdx.x & 31;
+    auto landed = [&](uint64_t& b, int parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag));
+    };
+    if (kv_mixed && landed(bars->kv_full, 0)) {
+      zero_tile_rows(sK, Cfg::kRegions, row1 - key0, 128);
+      zero_tile_rows(sV, Cfg::kRegions, row1 - key0, 128);
+      publish_rows(bar(bars->kv_clean));
+    }
+    for (int i = 0; i < ntiles; ++i) {
+      const int st = i & 1;
+      const bool mixed = mixed_tile(w, i);
+      int r0, r1;
+      own_tile_rows(a, w, i, r0, r1);
+      if (!landed(bars->q_full[st], (i >> 1) & 1)) break;
+      if (mixed) {
+        zero_tile_rows(sQ(st), Cfg::kRegions, 0, r0);
+        zero_tile_rows(sQ(st), Cfg::kRegions, r1, 128);
+        publish_rows(bar(bars->q_clean[i == 0 ? 0 : 1]));
+      }
+      if (lane == 0) mbar_arrive(bar(bars->q_empty[st]));
+      if (!landed(bars->do_full[st], (i >> 1) & 1)) break;
+      if (mixed) {
+        zero_tile_rows(sDO(st), Cfg::kRegions, 0, r0);
+        zero_tile_rows(sDO(st), Cfg::kRegions, r1, 128);
+        publish_rows(bar(bars->do_clean[i == 0 ? 0 : 1]));
+      }
+      if (lane == 0) mbar_arrive(bar(bars->do_empty[st]));
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ dQ warps 4-7
     // dQ of each tile is added to the fp32 accumulator by the TMA unit: the warps stage
@@ -976,6 +1088,13 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     for (int i = 0; i < ntiles; ++i) {
       const int t0q = (first_qt + i) * a.TQ;
+      // packed: a neighbour's rows of the tile get zeros (the bulk add covers whole tiles)
+      bool own = true;
+      if constexpr (kPacked) {
+        int r0, r1;
+        own_tile_rows(a, w, i, r0, r1);
+        own = r >= r0 && r < r1;
+      }
       mbar_wait(bar(bars->dq_full), i & 1, abort_flag);
       tc_fence_after();
 #pragma unroll 1
@@ -985,6 +1104,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
           uint32_t o[32];
           tmem_ld32(tS + lane_base + half * 64 + q * 32, o);
           tmem_wait_ld();
+          if (kPacked && !own) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
           const uint32_t reg = sDS + q * kBwdRegion + uint32_t(r) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -1049,6 +1172,7 @@ struct SeqHBars {
   uint64_t qdo_full[2], qdo_empty[2];  // Q, dO and row terms of a tile stage
   uint64_t s_full[2], pds_full[2], dq_full[2], dq_free[2];  // s_full: S and dP landed
   uint64_t kv_done, acc_zero;
+  uint64_t kv_clean, qdo_clean[2];  // packed: neighbours' rows zeroed
   uint32_t tmem_base;
   int abort;
   int lo_tile[2];  // half h of tile i needs its lo passes iff lo_tile[h] == i + 1
@@ -1072,16 +1196,19 @@ constexpr float kLoKeep = MODA_BWD_LO_KEEP;
 // consecutive columns of one row: 128 bytes).  Half row r is tile row R = 64h + r, i.e.
 // token R / G and head R % G.  GT = G for a power of two up to 16, so that each row's
 // offset from its head's base pointer is a compile-time constant; GT = 0 handles any G.
-template <int GT>
+// Packed: only the sequence's own rows of a tile are added to.
+template <int GT, bool kPacked>
 __device__ __forceinline__ void dq_readout(const SeqArgs& a, SeqHBars* bars, uint32_t tmem,
-                                           uint32_t lane_base, int c, int bg, int first_qt,
-                                           int ntiles) {
+                                           uint32_t lane_base, int c, int bg,
+                                           const SeqSpan& w) {
+  const int first_qt = w.first_qt, ntiles = w.ntiles;
   constexpr int D = 128;
   volatile int* abort_flag = &bars->abort;
   const long long hs = (long long)a.T * D;
   for (int i = 0; i < ntiles; ++i) {
     const int t0q = (first_qt + i) * a.TQ;
-    const int ntok = min(a.TQ, a.T - t0q);  // valid tokens of this tile
+    const int ntok = min(a.TQ, w.row1 - t0q);  // valid tokens of this tile
+    const int tlo = kPacked ? max(0, w.row0 - t0q) : 0;  // ... and the first of them
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       const uint32_t tA = tmem + uint32_t(64 * h);  // region A_h
@@ -1110,7 +1237,8 @@ __device__ __forceinline__ void dq_readout(const SeqArgs& a, SeqHBars* bars, uin
           for (int tk = 0; tk < 64 / GT; ++tk)
 #pragma unroll
             for (int j = 0; j < HB; ++j)
-              if (tk < nv) red_add_f32(ph[j] + tk * D, __uint_as_float(o[tk * GT + hb * HB + j]));
+              if (tk < nv && (!kPacked || tk >= tlo - tok0))
+                red_add_f32(ph[j] + tk * D, __uint_as_float(o[tk * GT + hb * HB + j]));
         }
       } else {
         float* const base = a.dqacc + ((long long)bg * a.G * a.T + t0q) * D + c;
@@ -1118,7 +1246,7 @@ __device__ __forceinline__ void dq_readout(const SeqArgs& a, SeqHBars* bars, uin
         for (int r = 0; r < 64; ++r) {
           const int R = 64 * h + r;
           const int tok = R / a.G;
-          if (tok < ntok)
+          if (tok < ntok && (!kPacked || tok >= tlo))
             red_add_f32(base + (R - tok * a.G) * hs + tok * D, __uint_as_float(o[r]));
         }
       }
@@ -1126,7 +1254,8 @@ __device__ __forceinline__ void dq_readout(const SeqArgs& a, SeqHBars* bars, uin
   }
 }
 
-__global__ void __launch_bounds__(kSeqHThreads, 1)
+template <bool kPacked>
+__global__ void __launch_bounds__(kSeqHThreads + (kPacked ? 32 : 0), 1)
     moda_bwd_seq_h_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmDO,
                           const __grid_constant__ CUtensorMap tmK,
@@ -1150,21 +1279,24 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int bg = blockIdx.x % a.BG;
-  const int kb = blockIdx.x / a.BG;
-  const int key0 = kb * 128;
-  const int first_qt = a.causal ? key0 / a.TQ : 0;
-  const int ntiles = a.nqt - first_qt;
+  SeqSpan w;
+  if (!seq_span<kPacked>(a, w)) return;
+  const int key0 = w.key0, row1 = w.row1, first_qt = w.first_qt, ntiles = w.ntiles;
+  const bool kv_mixed = kPacked && key0 + 128 > row1;  // the key block reaches past the end
 
   if (threadIdx.x == 0) {
     mbar_init(bar(bars->kv_full), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars->qdo_full[i]), 1);
-      mbar_init(bar(bars->qdo_empty[i]), 2);  // one commit from each issuer
+      // one commit from each issuer (packed: and warp 15 has seen it)
+      mbar_init(bar(bars->qdo_empty[i]), kPacked ? 3 : 2);
+      if (kPacked) mbar_init(bar(bars->qdo_clean[i]), 1);
       mbar_init(bar(bars->s_full[i]), 1);
       mbar_init(bar(bars->pds_full[i]), 256);
       mbar_init(bar(bars->dq_full[i]), 1);
       mbar_init(bar(bars->dq_free[i]), 128);
     }
+    if (kPacked) mbar_init(bar(bars->kv_clean), 1);
     mbar_init(bar(bars->kv_done), 2);
     mbar_init(bar(bars->acc_zero), 256);
     bars->abort = 0;
@@ -1235,10 +1367,15 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
       constexpr uint32_t idesc_t = make_idesc_bf16(128, 64, 0, 0);  // S^T_h, dP^T_h
       constexpr uint32_t idesc_g = make_idesc_bf16(128, D, 0, 1);   // dV, dK (A in TMEM)
       constexpr uint32_t idesc_q = make_idesc_bf16(128, 64, 1, 1);  // dQ^T_h = K^T dS_h^T
-      mbar_wait(bar(bars->kv_full), 0, abort_flag);
+      mbar_wait(bar(kv_mixed ? bars->kv_clean : bars->kv_full), 0, abort_flag);
       // S^T_h(i) = K Q_h(i)^T, dP^T_h(i) = V dO_h(i)^T : B = the half's 64 rows, K-major
+      // (a tile with a neighbour's rows, packed: until those are zeroed; the first and the
+      // last tile of the walk have a one-shot barrier each)
       auto wait_qdo = [&](int i) {
-        mbar_wait(bar(bars->qdo_full[i & 1]), (i >> 1) & 1, abort_flag);
+        if (kPacked && mixed_tile(w, i))
+          mbar_wait(bar(bars->qdo_clean[i == 0 ? 0 : 1]), 0, abort_flag);
+        else
+          mbar_wait(bar(bars->qdo_full[i & 1]), (i >> 1) & 1, abort_flag);
       };
       // (qdo_full of tile i waited for beforehand)
       auto issue_s = [&](int i, int h) {
@@ -1313,7 +1450,7 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
         // one early test for the next tile's Q and dO, while this half's P/dS is still
         // being computed: when they have landed, dP' below needs no wait of its own
         const bool qdo_seen =
-            i + 1 < ntiles &&
+            i + 1 < ntiles && !(kPacked && mixed_tile(w, i + 1)) &&
             mbar_try_wait(bar(bars->qdo_full[(i + 1) & 1]), ((i + 1) >> 1) & 1);
         issue_grads(i, h);
         tc_commit(bar(bars->qdo_empty[i & 1]));  // Q(i), dO(i): this half's products read
@@ -1354,7 +1491,7 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
       // The tile's row terms came with its Q and dO: the issuer saw them land (qdo_full)
       // before it issued S, and the s_full wait below orders them before the reads.
       int r_min = 0;
-      if (key >= a.T)
+      if (key >= row1)
         r_min = 1 << 30;
       else if (a.causal)
         r_min = a.G * (key - qt * a.TQ);
@@ -1479,7 +1616,7 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
     // epilogue: group 0 writes this key's dV row, group 1 its dK row
     mbar_wait(bar(bars->kv_done), 0, abort_flag);
     tc_fence_after();
-    const bool kvalid = key < a.T;
+    const bool kvalid = key < row1;
     const long long koff = ((long long)bg * a.T + (kvalid ? key : 0)) * D;
     {
       const uint32_t tsrc = (g ? tDK : tDV) + lane_base;
@@ -1501,6 +1638,39 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
         }
       }
     }
+  } else if (kPacked && warp == 15) {
+    // ------------------------------------------------------------ neighbours' rows
+    const int lane = threadIdx.x & 31;
+    auto landed = [&](uint64_t& b, int parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag));
+    };
+    if (kv_mixed && landed(bars->kv_full, 0)) {
+      zero_tile_rows(sK, Cfg::kRegions, row1 - key0, 128);
+      zero_tile_rows(sV, Cfg::kRegions, row1 - key0, 128);
+      publish_rows(bar(bars->kv_clean));
+    }
+    float* const rows = reinterpret_cast<float*>(smem + Cfg::kOffLD);
+    for (int i = 0; i < ntiles; ++i) {
+      const int st = i & 1;
+      if (!landed(bars->qdo_full[st], (i >> 1) & 1)) break;
+      if (mixed_tile(w, i)) {
+        int r0, r1;
+        own_tile_rows(a, w, i, r0, r1);
+        zero_tile_rows(sQ(st), Cfg::kRegions, 0, r0);
+        zero_tile_rows(sQ(st), Cfg::kRegions, r1, 128);
+        zero_tile_rows(sDO(st), Cfg::kRegions, 0, r0);
+        zero_tile_rows(sDO(st), Cfg::kRegions, r1, 128);
+        // row terms of weight zero (the records behind the last token were never written)
+        for (int r = lane; r < 128; r += 32)
+          if (r < r0 || r >= r1) {
+            rows[st * 256 + r] = -INFINITY;
+            rows[st * 256 + 128 + r] = 0.f;
+          }
+        publish_rows(bar(bars->qdo_clean[i == 0 ? 0 : 1]));
+      }
+      if (lane == 0) mbar_arrive(bar(bars->qdo_empty[st]));
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ dQ warps 8-11
     // Thread = TMEM lane = head-dimension index c of dQ^T_h: it reads its 64 row values,
@@ -1509,12 +1679,12 @@ __global__ void __launch_bounds__(kSeqHThreads, 1)
     const int c = threadIdx.x - 256;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     switch (a.G) {
-      case 1: dq_readout<1>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
-      case 2: dq_readout<2>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
-      case 4: dq_readout<4>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
-      case 8: dq_readout<8>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
-      case 16: dq_readout<16>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
-      default: dq_readout<0>(a, bars, tmem, lane_base, c, bg, first_qt, ntiles); break;
+      case 1: dq_readout<1, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
+      case 2: dq_readout<2, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
+      case 4: dq_readout<4, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
+      case 8: dq_readout<8, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
+      case 16: dq_readout<16, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
+      default: dq_readout<0, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
     }
   }
 
@@ -1539,6 +1709,24 @@ __global__ void __launch_bounds__(256) moda_dq_convert_kernel(const float* __res
   }
 }
 
+// The same for a packed batch, acc and dq [Hq][N][d] with d = 8 << shift: rows outside all
+// sequences are left as they are.
+__global__ void __launch_bounds__(256) moda_dq_convert_packed_kernel(
+    const float* __restrict__ acc, __nv_bfloat16* __restrict__ dq, long long n8, int shift, int N,
+    const int* __restrict__ cu, int nseq) {
+  int lo, hi;
+  packed_rows(cu, nseq, N, lo, hi);
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8;
+       i += (long long)gridDim.x * blockDim.x) {
+    const int t = int(unsigned(i >> shift) % unsigned(N));  // (at most 2^31 rows)
+    if (t < lo || t >= hi) continue;
+    const float4 x = reinterpret_cast<const float4*>(acc)[2 * i];
+    const float4 y = reinterpret_cast<const float4*>(acc)[2 * i + 1];
+    const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    reinterpret_cast<uint4*>(dq)[i] = pack8(f, 1.f);
+  }
+}
+
 // ============================================================ host side
 bool make_map_b(EncodeTiledFn encode, CUtensorMap* map, const void* base, int rank,
                 const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box) {
@@ -1556,8 +1744,8 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <int D, int GM, bool kRT>
-cudaError_t launch_depth(const BwdDepthArgs& args, cudaStream_t stream, const char** why) {
+template <int D, int GM, bool kRT, bool kPacked>
+cudaError_t launch_depth_as(const BwdDepthArgs& args, cudaStream_t stream, const char** why) {
   const int tpb = kDepthThreads / (D / 8);
   BwdDepthArgs a = args;
   // depth-only attention with q and dO in registers: stage the first pass's (P, <dO, vd>)
@@ -1568,23 +1756,31 @@ cudaError_t launch_depth(const BwdDepthArgs& args, cudaStream_t stream, const ch
                  : 0;
   // q/dO slots (not needed when they live in registers) + the per-thread cp.async ring
   const size_t smem = (GM <= 4 ? 0 : size_t(tpb) * 2 * a.G * D * 2) + kDepthRingBytes;
-  cudaError_t e = cudaFuncSetAttribute(moda_bwd_depth_kernel<D, GM, kRT>,
+  cudaError_t e = cudaFuncSetAttribute(moda_bwd_depth_kernel<D, GM, kRT, kPacked>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute(depth backward) failed";
     return e;
   }
   int per_sm = 1;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moda_bwd_depth_kernel<D, GM, kRT>,
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moda_bwd_depth_kernel<D, GM, kRT, kPacked>,
                                                 kDepthThreads, smem);
   if (per_sm < 1) per_sm = 1;
   const long long need = (a.ntok + tpb - 1) / tpb;
   const long long cap = (long long)sm_count() * per_sm;
   const unsigned grid = unsigned(need < cap ? need : cap);
-  moda_bwd_depth_kernel<D, GM, kRT><<<grid, kDepthThreads, smem, stream>>>(a);
+  moda_bwd_depth_kernel<D, GM, kRT, kPacked><<<grid, kDepthThreads, smem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) *why = "depth backward launch failed";
   return e;
+}
+
+template <int D, int GM, bool kRT>
+cudaError_t launch_depth(const BwdDepthArgs& a, cudaStream_t stream, const char** why) {
+  // (packed batches always have a sequence part, whose d = 128 kernel reads the records)
+  if constexpr (kRT || D == 64)
+    if (a.cu) return launch_depth_as<D, GM, kRT, true>(a, stream, why);
+  return launch_depth_as<D, GM, kRT, false>(a, stream, why);
 }
 
 // Byte offsets of the backward's workspace regions: the fp32 dq accumulator [B][Hq][T][d]
@@ -1649,6 +1845,8 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
   da.staged = 0;  // (decided per launch in launch_depth)
   da.scale = p.scale;
   da.scale_log2 = p.scale * kLog2eBwd;
+  da.cu = p.cu;
+  da.nseq = p.nseq;
   cudaError_t e = cudaSuccess;
   if (stages & kStageDepth) {
     auto launch = [&]() {
@@ -1726,16 +1924,26 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
     sa.causal = p.causal;
     sa.scale = p.scale;
     sa.scale_log2 = p.scale * kLog2eBwd;
-    const int nkb = (p.T + 127) / 128;
+    sa.cu = p.cu;
+    sa.nseq = p.nseq;
+    const unsigned nkb =
+        unsigned(p.cu ? packed_pieces_bound(p.T, p.nseq, 128) : (p.T + 127) / 128);
     if constexpr (D == 128) {
-      e = cudaFuncSetAttribute(moda_bwd_seq_h_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SeqCfg<128>::kSmemBytes);
-      if (e != cudaSuccess) {
-        *why = "cudaFuncSetAttribute(sequence backward, halves) failed";
-        return e;
-      }
-      moda_bwd_seq_h_kernel<<<unsigned(BG) * nkb, kSeqHThreads, SeqCfg<128>::kSmemBytes,
-                              stream>>>(mQ, mDO, mK, mV, sa);
+      auto run = [&](auto kernel, int threads) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SeqCfg<128>::kSmemBytes);
+        if (e != cudaSuccess) {
+          *why = "cudaFuncSetAttribute(sequence backward, halves) failed";
+          return;
+        }
+        kernel<<<unsigned(BG) * nkb, threads, SeqCfg<128>::kSmemBytes, stream>>>(mQ, mDO, mK, mV,
+                                                                                 sa);
+      };
+      if (p.cu)
+        run(moda_bwd_seq_h_kernel<true>, kSeqHThreads + 32);
+      else
+        run(moda_bwd_seq_h_kernel<false>, kSeqHThreads);
+      if (e != cudaSuccess) return e;
     } else {
       CUtensorMap mDQ;
       // fp32 dq accumulator viewed like q: [bg][t][head-in-group][c]; a box is 32 columns
@@ -1752,15 +1960,21 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
         *why = "cuTensorMapEncodeTiled failed for the dq accumulator";
         return cudaErrorInvalidValue;
       }
-      e = cudaFuncSetAttribute(moda_bwd_seq_kernel<D>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SeqCfg<D>::kSmemBytes);
-      if (e != cudaSuccess) {
-        *why = "cudaFuncSetAttribute(sequence backward) failed";
-        return e;
-      }
-      moda_bwd_seq_kernel<D><<<unsigned(BG) * nkb, kSeqThreads, SeqCfg<D>::kSmemBytes, stream>>>(
-          mQ, mDO, mK, mV, mDQ, sa);
+      auto run = [&](auto kernel, int threads) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SeqCfg<D>::kSmemBytes);
+        if (e != cudaSuccess) {
+          *why = "cudaFuncSetAttribute(sequence backward) failed";
+          return;
+        }
+        kernel<<<unsigned(BG) * nkb, threads, SeqCfg<D>::kSmemBytes, stream>>>(mQ, mDO, mK, mV,
+                                                                               mDQ, sa);
+      };
+      if (p.cu)
+        run(moda_bwd_seq_kernel<D, true>, kSeqThreads + 32);
+      else
+        run(moda_bwd_seq_kernel<D, false>, kSeqThreads);
+      if (e != cudaSuccess) return e;
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) {
@@ -1774,8 +1988,12 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
   const long long n8 = rows * D / 8;
   long long blocks = (n8 + 255) / 256;
   if (blocks > 8LL * sm_count()) blocks = 8LL * sm_count();
-  moda_dq_convert_kernel<<<unsigned(blocks), 256, 0, stream>>>(
-      dqacc, static_cast<__nv_bfloat16*>(dq), n8);
+  if (p.cu)
+    moda_dq_convert_packed_kernel<<<unsigned(blocks), 256, 0, stream>>>(
+        dqacc, static_cast<__nv_bfloat16*>(dq), n8, D == 128 ? 4 : 3, p.T, p.cu, p.nseq);
+  else
+    moda_dq_convert_kernel<<<unsigned(blocks), 256, 0, stream>>>(
+        dqacc, static_cast<__nv_bfloat16*>(dq), n8);
   e = cudaGetLastError();
   if (e != cudaSuccess) *why = "dq convert launch failed";
   return e;

@@ -40,6 +40,14 @@
 //            tile.  Because S_t(j+1) is issued after PV_t(j), a tile's warps that have
 //            seen S_t(j+1) know PV_t(j) has finished, so rescaling O_t needs no extra wait.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
+//
+// Packed batches (template flag kPacked): sequences of different lengths lie one behind the
+// other in one token axis of N rows.  A CTA's pair of tiles belongs to one sequence (found by
+// packed_find), whose first row is added to every coordinate; the rest of the kernel sees a
+// problem of that sequence's length.  A sequence's last V block and last depth blocks reach
+// into the rows behind it; warp 10 follows the ring and zeroes those rows of V and vd before
+// the tensor cores may read them (K, kd and Q need no zeroing: what they bring only enters
+// masked scores and rows that are not stored).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,6 +57,7 @@
 
 #include "moda_internal.h"
 #include "sm100.cuh"
+#include "moda_packed.cuh"
 
 namespace moda {
 
@@ -88,6 +97,7 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 constexpr int kFwdThreads = 320;
+constexpr int kFwdPackedThreads = kFwdThreads + 32;  // and warp 10, which zeroes rows
 
 // kDense selects the depth path: false = CUDA-core fold from two depth rings, true =
 // depth blocks through the K/V ring on the tensor cores (see the kernel comment).
@@ -111,6 +121,8 @@ struct FwdArgs {
   int B, Hq, Hkv, T, L, G, TQ, JC, nqt, npairs, causal;
   int depth_only;  // no sequence blocks: each row attends to its own token's depth only
   float scale_log2;
+  const int* cu;  // packed: [nseq + 1] first rows of the sequences (T is the row count N)
+  int nseq;
 };
 
 struct Bars {
@@ -124,6 +136,7 @@ struct Bars {
   uint64_t p_full[2];     // P_t(j) in TMEM (and O_t rescaled)
   uint64_t o_final[2];    // last PV_t done
   uint64_t drain;         // abort path: every product issued so far has finished
+  uint64_t clean[8];      // packed: K/V ring stage zeroed behind the sequence's last row
   uint32_t tmem_base;
   int abort;
 };
@@ -185,8 +198,8 @@ __device__ __forceinline__ float dot8(const float (&a)[8], uint4 w) {
   return s;
 }
 
-template <int D, bool kDense>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+template <int D, bool kDense, bool kPacked>
+__global__ void __launch_bounds__(kPacked ? kFwdPackedThreads : kFwdThreads, 1)
     moda_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV,
@@ -209,14 +222,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int nbg = a.B * a.Hkv;
   const int bg = blockIdx.x % nbg;
-  const int pair = a.npairs - 1 - blockIdx.x / nbg;  // heaviest (latest) pairs first
+  // heaviest (latest) pairs first; T and row0: this sequence's length and first row
+  int pair = a.npairs - 1 - int(blockIdx.x) / nbg, T = a.T, row0 = 0;
+  if constexpr (kPacked) {
+    const PackedPiece pc = packed_find(a.cu, a.nseq, a.T, 2 * a.TQ, int(blockIdx.x) / nbg);
+    if (!pc.found) return;  // the grid is sized by an upper bound
+    pair = pc.p;
+    T = pc.len;
+    row0 = pc.first;
+  }
   const int tq0 = 2 * pair * a.TQ, tq1 = tq0 + a.TQ;  // first token of tile 0 / tile 1
   const int NB0 =
-      a.depth_only ? 0 : ((a.causal ? min(a.T, tq0 + a.TQ) : a.T) + kBN - 1) / kBN;
+      a.depth_only ? 0 : ((a.causal ? min(T, tq0 + a.TQ) : T) + kBN - 1) / kBN;
   // NB0 <= NB1; a tile 1 past the end of the sequence is computed but never stored
-  const int NB1 = (tq1 >= a.T || a.depth_only)
+  const int NB1 = (tq1 >= T || a.depth_only)
                       ? NB0
-                      : ((a.causal ? min(a.T, tq1 + a.TQ) : a.T) + kBN - 1) / kBN;
+                      : ((a.causal ? min(T, tq1 + a.TQ) : T) + kBN - 1) / kBN;
   const bool has_depth = a.L > 0;
   const int nchunk = has_depth ? (a.L + a.JC - 1) / a.JC : 0;
   const int NC = kDense ? 0 : nchunk;  // CUDA-core fold chunks
@@ -228,12 +249,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   // vd of tile 1; sequence block: K then V, shared by both tiles.
   auto kidx = [&](int t, int j) { return sm.entry(j) + (sm.is_depth(j) ? t : 0); };
   auto vidx = [&](int t, int j) { return sm.entry(j) + (sm.is_depth(j) ? 2 + t : 1); };
+  // packed: first row of step j's value tile (of tile t, for a depth step) that lies behind
+  // the sequence, 128 when there is none.  (A tile 1 that is all behind it is never stored.)
+  auto clean_from = [&](int t, int j) {
+    if (!kPacked) return 128;
+    if (sm.is_depth(j)) {
+      const int left = T - (t ? tq1 : tq0);  // tokens of the tile inside the sequence
+      return left > 0 && left < a.TQ ? left * a.JC : 128;
+    }
+    return min(128, T - sm.index(j) * kBN);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(bars->q_full), 1);
     for (int s = 0; s < NKV; ++s) {
       mbar_init(bar(bars->full[s]), 1);
-      mbar_init(bar(bars->empty[s]), 1);
+      mbar_init(bar(bars->empty[s]), kPacked ? 2 : 1);  // packed: warp 10 has seen it too
+      if (kPacked) mbar_init(bar(bars->clean[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
       for (int s = 0; s < NDS; ++s) {
@@ -282,7 +314,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int t = 0; t < 2; ++t)
         for (int rg = 0; rg < Cfg::kRegions; ++rg)
           tma_load_4d(sQ(t) + rg * kRegion, &tmQ, bar(bars->q_full), rg * 64, 0,
-                      t ? tq1 : tq0, bg);
+                      row0 + (t ? tq1 : tq0), bg);
       int e = 0;  // ring entry
       // next ring stage, or -1 once a wait for a free stage has failed (the CTA aborts)
       auto acquire = [&](int bytes) {
@@ -304,7 +336,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const CUtensorMap* map = (u < 2) ? &tmKD : &tmVD;
             for (int rg = 0; rg < Cfg::kRegions; ++rg)
               tma_load_4d(sKV(s) + rg * kRegion, map, bar(bars->full[s]), rg * 64,
-                          ix * a.JC, (u & 1) ? tq1 : tq0, bg);
+                          ix * a.JC, row0 + ((u & 1) ? tq1 : tq0), bg);
           }
         } else {
           for (int u = 0; u < 2 && !stop; ++u) {
@@ -312,8 +344,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (s < 0) { stop = true; break; }
             const CUtensorMap* map = u ? &tmV : &tmK;
             for (int rg = 0; rg < Cfg::kRegions; ++rg)
-              tma_load_3d(sKV(s) + rg * kRegion, map, bar(bars->full[s]), rg * 64, ix * kBN,
-                          bg);
+              tma_load_3d(sKV(s) + rg * kRegion, map, bar(bars->full[s]), rg * 64,
+                          row0 + ix * kBN, bg);
           }
         }
       }
@@ -346,14 +378,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int idx = 0; idx < kDPrefetch && idx < nuse; ++idx) {
         const CUtensorMap* map; int x, y;
         box(idx, map, x, y);
-        tma_prefetch_l2_4d(map, x, y, t ? tq1 : tq0, bg);
+        tma_prefetch_l2_4d(map, x, y, row0 + (t ? tq1 : tq0), bg);
       }
       int issued = 0;
       for (int idx = 0; idx < nuse; ++idx) {
         if (idx + kDPrefetch < nuse) {
           const CUtensorMap* pmap; int px, py;
           box(idx + kDPrefetch, pmap, px, py);
-          tma_prefetch_l2_4d(pmap, px, py, t ? tq1 : tq0, bg);
+          tma_prefetch_l2_4d(pmap, px, py, row0 + (t ? tq1 : tq0), bg);
         }
         const int s = idx % NDS;
         if (idx >= NDS &&
@@ -364,7 +396,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int rg = u % Cfg::kRegions;
         mbar_expect_tx(bar(bars->dfull[t][s]), dbytes);
         tma_load_4d(sDS(t, s), map, bar(bars->dfull[t][s]), rg * 64, (idx / kDUses) * a.JC,
-                    t ? tq1 : tq0, bg);
+                    row0 + (t ? tq1 : tq0), bg);
         issued = idx + 1;
       }
       if (*abort_flag) {
@@ -406,10 +438,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_commit(bar(bars->s_full[t]));
         if (sm.is_depth(j) || t == 1) release(e);
       };
+      uint32_t clean_parity = 0;  // bit s: parity of stage s's next zeroing
       auto issue_pv = [&](int t, int j) {
         const int e = vidx(t, j);
         // V's entry first: it has normally landed long before P is ready
-        if (!seen_by_tile0(t, j)) wait_entry(e);
+        if (!seen_by_tile0(t, j)) {
+          if (kPacked && clean_from(t, j) < 128) {
+            const int s = e % NKV;
+            mbar_wait(bar(bars->clean[s]), (clean_parity >> s) & 1u, abort_flag);
+            clean_parity ^= 1u << s;
+            tc_fence_after();
+          } else {
+            wait_entry(e);
+          }
+        }
         const uint32_t vbase = sKV(e % NKV);
         const uint32_t tO = tmem + 256 + t * D;
         // keys [0, 64) as soon as their P is in (while the warps compute the rest), then
@@ -450,6 +492,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     }
     __syncwarp();
+  } else if (kPacked && warp == 10) {
+    // ------------------------------------------------------------ rows behind the sequence
+    // Follows every ring entry in order (and so holds each stage until it has seen it, which
+    // keeps its parities in step) and zeroes the value rows behind the sequence's last one.
+    int e = 0;
+    bool stop = false;
+    for (int j = 0; j < N1 && !stop; ++j) {
+      const int nu = sm.is_depth(j) ? 4 : 2;
+      for (int u = 0; u < nu && !stop; ++u, ++e) {
+        const int s = e % NKV;
+        stop = !__all_sync(0xffffffffu, mbar_wait(bar(bars->full[s]), (e / NKV) & 1, abort_flag));
+        if (stop) break;
+        const bool values = nu == 4 ? u >= 2 : u == 1;
+        const int r0 = values ? clean_from(u & 1, j) : 128;
+        if (r0 < 128) {
+          zero_tile_rows(sKV(s), Cfg::kRegions, r0, 128);
+          publish_rows(bar(bars->clean[s]));
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar(bars->empty[s]));
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ compute warps
     const int tt = warp >> 2;                     // tile of this warpgroup
@@ -458,7 +523,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int hl = r - tok * a.G;
     const int t0 = tt ? tq1 : tq0;
     const int t = t0 + tok;
-    const bool valid = (tok < a.TQ) && (t < a.T);
+    const bool valid = (tok < a.TQ) && (t < T);
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + tt * 128;
     const uint32_t tO = tmem + lane_base + 256 + tt * D;
@@ -555,7 +620,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // A depth step's 128 keys are JC = G entries of each of the tile's TQ tokens,
     // token-major, so row r (token r / G) owns keys [r - hl, r - hl + G): all inside the
     // 32 keys of its warp's rows.  Only those 32 columns are read; P is zero elsewhere.
-    const int key_lim = a.causal ? t : a.T - 1;
+    const int key_lim = a.causal ? t : T - 1;
     // Steps before K(R+1) may be either kind; then come the remaining depth steps, then
     // sequence blocks only.  Each run has its own copy of the loop body, without the code
     // of the kind it never meets, which keeps the hot loop small.
@@ -587,7 +652,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_wait_ld();
         const int kbase = ix * kBN;
         const bool need_mask =
-            kind != 0 && (a.causal ? (kbase + kBN - 1 > t0) : (kbase + kBN > a.T));
+            kind != 0 && (a.causal ? (kbase + kBN - 1 > t0) : (kbase + kBN > T));
         if (need_mask) {
 #pragma unroll
           for (int c = 0; c < kBN; ++c)
@@ -702,7 +767,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int J1 = kDense ? min(NS, J0 + (sm.ND - sm.K)) : 0;
     // From J1 on, step j is sequence block j - J1 + K*R.  Blocks from ix_m on may hold
     // keys past a row's token (causal) or past the end; the blocks before it need no mask.
-    const int ix_m = a.causal ? (t0 + 1) / kBN : a.T / kBN;
+    const int ix_m = a.causal ? (t0 + 1) / kBN : T / kBN;
     const int JM = min(NS, J1 + max(0, ix_m - (kDense ? sm.K * sm.R : 0)));
 #pragma unroll 1
     for (int jb = 0; jb < J0; ++jb) run_step(jb, std::integral_constant<int, 2>{});
@@ -719,7 +784,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const float inv_l = 1.f / l;
     const int h = (bg % a.Hkv) * a.G + hl;
     const int b = bg / a.Hkv;
-    const size_t row_off = ((size_t(b) * a.Hq + h) * a.T + (valid ? t : 0)) * D;
+    const size_t row_off = ((size_t(b) * a.Hq + h) * a.T + row0 + (valid ? t : 0)) * D;
 #pragma unroll
     for (int cc = 0; cc < D / 32; ++cc) {
       uint32_t o[32];
@@ -742,7 +807,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
     }
-    if (valid) a.lse[(size_t(b) * a.Hq + h) * a.T + t] = (m + __log2f(l)) * kLn2;
+    if (valid) a.lse[(size_t(b) * a.Hq + h) * a.T + row0 + t] = (m + __log2f(l)) * kLn2;
   }
 
   tc_fence_before();
@@ -765,7 +830,7 @@ bool make_map(EncodeTiledFn encode, CUtensorMap* map, const void* base, int rank
   return r == CUDA_SUCCESS;
 }
 
-template <int D, bool kDense>
+template <int D, bool kDense, bool kPacked>
 cudaError_t launch_forward_d(const Problem& p, const void* q, const void* k, const void* v,
                              const void* kd, const void* vd, void* out, float* lse,
                              EncodeTiledFn encode, cudaStream_t stream, const char** why) {
@@ -829,9 +894,11 @@ cudaError_t launch_forward_d(const Problem& p, const void* q, const void* k, con
   args.causal = p.causal;
   args.depth_only = p.depth_only;
   args.scale_log2 = p.scale * kLog2e;
+  args.cu = p.cu;
+  args.nseq = p.nseq;
 
   {
-    cudaError_t e = cudaFuncSetAttribute(moda_fwd_kernel<D, kDense>,
+    cudaError_t e = cudaFuncSetAttribute(moda_fwd_kernel<D, kDense, kPacked>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Cfg::kSmemBytes);
     if (e != cudaSuccess) {
@@ -839,9 +906,12 @@ cudaError_t launch_forward_d(const Problem& p, const void* q, const void* k, con
       return e;
     }
   }
-  const unsigned grid = unsigned(BG) * unsigned(args.npairs);
-  moda_fwd_kernel<D, kDense><<<grid, kFwdThreads, Cfg::kSmemBytes, stream>>>(
-      mQ, mK, mV, mKD, mVD, args);
+  const unsigned grid =
+      unsigned(BG) *
+      unsigned(kPacked ? packed_pieces_bound(p.T, p.nseq, 2 * tg.TQ) : args.npairs);
+  moda_fwd_kernel<D, kDense, kPacked>
+      <<<grid, kPacked ? kFwdPackedThreads : kFwdThreads, Cfg::kSmemBytes, stream>>>(
+          mQ, mK, mV, mKD, mVD, args);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) *why = "forward kernel launch failed";
   return e;
@@ -881,11 +951,19 @@ cudaError_t launch_forward(const Problem& p, const void* q, const void* k, const
                            const char** why) {
   const bool dense = depth_path == kDepthPathDense ||
                      (depth_path == kDepthPathAuto && dense_depth_default(p));
-  if (p.d == 128)
-    return dense ? launch_forward_d<128, true>(p, q, k, v, kd, vd, out, lse, encode, stream, why)
-                 : launch_forward_d<128, false>(p, q, k, v, kd, vd, out, lse, encode, stream, why);
-  return dense ? launch_forward_d<64, true>(p, q, k, v, kd, vd, out, lse, encode, stream, why)
-               : launch_forward_d<64, false>(p, q, k, v, kd, vd, out, lse, encode, stream, why);
+  auto launch = [&](auto packed_c) {
+    constexpr bool kP = decltype(packed_c)::value;
+    if (p.d == 128)
+      return dense ? launch_forward_d<128, true, kP>(p, q, k, v, kd, vd, out, lse, encode,
+                                                     stream, why)
+                   : launch_forward_d<128, false, kP>(p, q, k, v, kd, vd, out, lse, encode,
+                                                      stream, why);
+    return dense
+               ? launch_forward_d<64, true, kP>(p, q, k, v, kd, vd, out, lse, encode, stream, why)
+               : launch_forward_d<64, false, kP>(p, q, k, v, kd, vd, out, lse, encode, stream,
+                                                 why);
+  };
+  return p.cu ? launch(std::true_type{}) : launch(std::false_type{});
 }
 
 }  // namespace moda

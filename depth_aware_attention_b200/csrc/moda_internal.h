@@ -14,6 +14,10 @@ struct Problem {
   int causal;
   float scale;
   int depth_only = 0;  // 1: no sequence keys (depth-only attention); k, v unused
+  // packed batch: B = 1, T = all token rows, sequence s in rows [cu[s], cu[s+1]) (device
+  // array of nseq + 1); null: every sequence has T tokens
+  const int* cu = nullptr;
+  int nseq = 0;
 };
 
 // Tile geometry shared by the kernels: a query tile holds 128 (token, head) rows, TQ

@@ -131,6 +131,45 @@ moda_status_t moda_depth_attention_backward(const void *q, const void *kd, const
                                             moda_stream_t stream);
 
 /*
+ * Forward over a packed batch: nseq sequences of different lengths lie one behind the other
+ * in ONE token axis of N rows, and every query attends, in one joint softmax, to its own
+ * sequence's keys and to its own token's L depth keys.  (The pages describe equal lengths;
+ * this is the same definition applied to each sequence by itself.)
+ *   q, out: bf16 [Hq][N][d]    k, v: bf16 [Hkv][N][d]    kd, vd: bf16 [Hkv][N][L][d]
+ *   lse: fp32 [Hq][N]          cu_seqlens: int32 [nseq + 1], a DEVICE array, 4-byte aligned:
+ *   sequence s is the rows [cu_seqlens[s], cu_seqlens[s+1]); a length may be 0.
+ * causal != 0: token t of a sequence sees its keys s <= t; causal == 0: all of them.
+ * Rows before cu_seqlens[0] and from cu_seqlens[nseq] on belong to no sequence: they are
+ * neither read into any result (whatever bits they hold) nor written in out and lse.  No
+ * value of one sequence reaches another's results either.  Within a sequence every value
+ * must be finite.
+ * The entries must not decrease and must lie in [0, N].  They are known on the device alone:
+ * a sequence whose two entries break this is treated as empty and sets bit 2 of the device
+ * error word (moda_check_device_errors() returns MODA_ERR_INTERNAL).  The lengths are read
+ * when the kernel runs, so a captured graph follows them.
+ * nseq >= 1, N >= 1, scale > 0; everything else as moda_forward.  One launch, no workspace.
+ */
+moda_status_t moda_forward_packed(const void *q, const void *k, const void *v, const void *kd,
+                                  const void *vd, const int32_t *cu_seqlens, void *out,
+                                  float *lse, int Hq, int Hkv, int N, int nseq, int L, int d,
+                                  float scale, int causal, moda_stream_t stream);
+
+/*
+ * Gradients of sum(out * dout) over a packed batch: moda_backward's, per sequence, in the
+ * layouts of moda_forward_packed (whose out and lse it takes).  The gradients' rows outside
+ * all sequences are left as they are, and those of the inputs, out, lse and dout are not
+ * read into any result.  Workspace: moda_backward_workspace_size(1, Hq, Hkv, N, L, d) bytes.
+ * Summation order, launches and everything else as moda_backward.
+ */
+moda_status_t moda_backward_packed(const void *q, const void *k, const void *v, const void *kd,
+                                   const void *vd, const int32_t *cu_seqlens, const void *out,
+                                   const float *lse, const void *dout, void *dq, void *dk,
+                                   void *dv, void *dkd, void *dvd, void *workspace,
+                                   size_t workspace_bytes, int Hq, int Hkv, int N, int nseq,
+                                   int L, int d, float scale, int causal,
+                                   moda_stream_t stream);
+
+/*
  * Single-token decode: the forward's row for the newest token of each sequence.  The
  * K/V cache holds S sequence keys/values, the last of them the newest token's own; its
  * query row sees all S of them (the causal row of position S-1) and its own L depth
