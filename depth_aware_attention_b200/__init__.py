@@ -32,6 +32,7 @@ BACKWARD_LAUNCHES = 3
 EXPORTED = ("moda_forward", "moda_forward_depth_path", "moda_depth_attention_forward",
             "moda_depth_attention_backward", "moda_decode", "moda_decode_workspace_size",
             "moda_depth_kv_write", "moda_forward_packed", "moda_backward_packed",
+            "moda_tree_decode", "moda_tree_decode_workspace_size",
             "moda_backward", "moda_backward_workspace_size",
             "moda_backward_stages", "moda_backward_noalloc", "moda_check_device_errors",
             "moda_test_set_device_fault", "moda_test_exp2_fma", "moda_status_string",
@@ -77,6 +78,10 @@ def _load():
     lib.moda_forward_packed.restype = I
     lib.moda_backward_packed.argtypes = [P] * 15 + [S] + [I] * 6 + [F, I, P]
     lib.moda_backward_packed.restype = I
+    lib.moda_tree_decode_workspace_size.argtypes = [I] * 7
+    lib.moda_tree_decode_workspace_size.restype = S
+    lib.moda_tree_decode.argtypes = [P] * 12 + [S] + [I] * 7 + [F, P]
+    lib.moda_tree_decode.restype = I
     lib.moda_test_set_device_fault.argtypes = [I, ctypes.c_uint64]
     lib.moda_test_set_device_fault.restype = I
     lib.moda_test_exp2_fma.argtypes = [P, P, I, P]
@@ -183,6 +188,17 @@ def moda_backward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, dout, dq, dk, dv
     return lib.moda_backward_packed(q, k, v, kd, vd, cu_seqlens, out, lse, dout, dq, dk, dv,
                                     dkd, dvd, workspace, workspace_bytes, Hq, Hkv, N, nseq, L,
                                     d, float(scale), int(causal), stream)
+
+
+def moda_tree_decode_workspace_size(B, Hq, Hkv, S, N, L, d):
+    return lib.moda_tree_decode_workspace_size(B, Hq, Hkv, S, N, L, d)
+
+
+def moda_tree_decode(q, k, v, kt, vt, kd, vd, parents, lengths, out, lse, workspace,
+                     workspace_bytes, B, Hq, Hkv, S, N, L, d, scale, stream):
+    """Direct call of moda_tree_decode with raw pointers (ints) and a stream handle."""
+    return lib.moda_tree_decode(q, k, v, kt, vt, kd, vd, parents, lengths, out, lse, workspace,
+                                workspace_bytes, B, Hq, Hkv, S, N, L, d, float(scale), stream)
 
 
 def moda_backward_workspace_size(B, Hq, Hkv, T, L, d):
@@ -594,3 +610,44 @@ def backward_packed(q, k, v, cu_seqlens, kd, vd, out, lse, dout, scale=None, cau
           _at(dout), _at(g["dq"]), _at(g["dk"]), _at(g["dv"]), _at(g["dkd"]), _at(g["dvd"]),
           _at(workspace), _nbytes(workspace), Hq, Hkv, N, nseq, L, d, scale, 1 if causal else 0)
     return g
+
+
+def tree_decode(q, k, v, kt, vt, parents, lengths, kd=None, vd=None, scale=None, out=None,
+                lse=None, workspace=None):
+    """Attention of N drafted tokens per sequence over a ragged cache, on the current CUDA
+    stream.  Returns (out [B,Hq,N,d] bf16, lse [B,Hq,N] fp32).
+
+    q [B,Hq,N,d]; cache k/v [B,Hkv,S,d] with lengths int32 [B] keys in use; the new tokens'
+    own kt/vt [B,Hkv,N,d] and depth entries kd/vd [B,Hkv,N,L,d] (or None for L = 0); parents
+    int32 [B,N]: each new token's parent, -1 for a child of the cache's last token, -2 for an
+    unused slot (out 0, lse -inf).  N = 1 is single-token decoding.
+    """
+    import torch
+    _ndim("q", q, 4)
+    _ndim("k", k, 4)
+    if kd is not None:
+        _ndim("kd", kd, 5)
+    B, Hq, N, d = q.shape
+    Hkv, S = k.shape[1], k.shape[2]
+    L = 0 if kd is None else kd.shape[3]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq, N), device=q.device, dtype=torch.float32)
+    if workspace is None:
+        workspace = torch.empty(lib.moda_tree_decode_workspace_size(B, Hq, Hkv, S, N, L, d),
+                                device=q.device, dtype=torch.uint8)
+    bf, new = torch.bfloat16, (B, Hkv, N, d)
+    spec = [("q", q, (B, Hq, N, d), bf), ("k", k, (B, Hkv, S, d), bf), ("v", v, (B, Hkv, S, d), bf),
+            ("kt", kt, new, bf), ("vt", vt, new, bf), ("parents", parents, (B, N), torch.int32),
+            ("lengths", lengths, (B,), torch.int32), ("out", out, (B, Hq, N, d), bf),
+            ("lse", lse, (B, Hq, N), torch.float32)]
+    if L:
+        spec += [("kd", kd, (B, Hkv, N, L, d), bf), ("vd", vd, (B, Hkv, N, L, d), bf)]
+    _checked(q.device, spec, workspace)
+    _call(lib.moda_tree_decode, "moda_tree_decode", q.device, _at(q), _at(k), _at(v), _at(kt),
+          _at(vt), _at(kd) if L else None, _at(vd) if L else None, _at(parents), _at(lengths),
+          _at(out), _at(lse), _at(workspace), _nbytes(workspace), B, Hq, Hkv, S, N, L, d, scale)
+    return out, lse

@@ -67,6 +67,52 @@ moda_status_t check_packed(const int* cu, int nseq, int Hq, int Hkv, int N, floa
   return MODA_OK;
 }
 
+// Sizes of the ragged-cache entry points: N query tokens per sequence over a cache of up to S
+// keys.  (The cache itself is only addressed by coordinates or 64-bit offsets, so the number
+// of its rows has no 32-bit limit.)
+moda_status_t check_cache_sizes(int B, int Hq, int Hkv, int S, int N, int L, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || S < 1 || N < 1 || L < 0)
+    return fail(MODA_ERR_INVALID_ARGUMENT, "sizes must satisfy B,Hq,Hkv,S,N >= 1 and L >= 0");
+  if (Hq % Hkv != 0) return fail(MODA_ERR_INVALID_ARGUMENT, "Hq must be a multiple of Hkv");
+  if (d != 64 && d != 128) return fail(MODA_ERR_UNSUPPORTED, "head size d must be 64 or 128");
+  if (Hq / Hkv > 64) return fail(MODA_ERR_UNSUPPORTED, "query heads per KV head must be <= 64");
+  if (N > 128) return fail(MODA_ERR_UNSUPPORTED, "query tokens per sequence must be <= 128");
+  if (1LL * B * Hq * N > (1LL << 30) || 1LL * B * Hkv > 65535 || S > (1 << 30) || L > 65535)
+    return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");
+  return MODA_OK;
+}
+
+// A buffer of a call, for the checks that every entry point makes of its pointers.
+struct Buf {
+  const void* p;
+  size_t bytes;
+  unsigned align;
+};
+
+// Non-NULL (unless empty), aligned, and no output overlapping an input or another output.
+template <int NI, int NO>
+moda_status_t check_buffers(const Buf (&in)[NI], const Buf (&out)[NO]) {
+  for (const Buf& b : in) {
+    if (b.bytes && !b.p) return fail(MODA_ERR_INVALID_ARGUMENT, "an input pointer is NULL");
+    if (b.p && reinterpret_cast<uintptr_t>(b.p) % b.align)
+      return fail(MODA_ERR_INVALID_ARGUMENT, "an input pointer is misaligned");
+  }
+  for (const Buf& b : out) {
+    if (b.bytes && !b.p) return fail(MODA_ERR_INVALID_ARGUMENT, "an output pointer is NULL");
+    if (b.p && reinterpret_cast<uintptr_t>(b.p) % b.align)
+      return fail(MODA_ERR_INVALID_ARGUMENT, "an output pointer is misaligned");
+  }
+  for (int o = 0; o < NO; ++o) {
+    for (const Buf& b : in)
+      if (overlaps(out[o].p, out[o].bytes, b.p, b.bytes))
+        return fail(MODA_ERR_INVALID_ARGUMENT, "an output overlaps an input");
+    for (int o2 = o + 1; o2 < NO; ++o2)
+      if (overlaps(out[o].p, out[o].bytes, out[o2].p, out[o2].bytes))
+        return fail(MODA_ERR_INVALID_ARGUMENT, "two outputs overlap");
+  }
+  return MODA_OK;
+}
+
 // Device check, cached per device: compute capability 10.x (B200 / sm_100a).
 moda_status_t check_device() {
   int dev = 0;
@@ -305,6 +351,54 @@ moda_status_t moda_decode(const void* q, const void* k, const void* v, const voi
   const char* why = "";
   cudaError_t e = moda::launch_decode(p, q, k, v, kd, vd, out, lse, workspace, enc,
                                       static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) {
+    snprintf(g_msg, sizeof(g_msg), "%s: %s", why, cudaGetErrorString(e));
+    return MODA_ERR_CUDA;
+  }
+  return MODA_OK;
+}
+
+size_t moda_tree_decode_workspace_size(int B, int Hq, int Hkv, int S, int N, int L, int d) {
+  if (check_cache_sizes(B, Hq, Hkv, S, N, L, d) != MODA_OK) return 0;
+  return moda::tree_workspace_bytes(moda::TreeProblem{B, Hq, Hkv, S, N, L, d, 1.f});
+}
+
+moda_status_t moda_tree_decode(const void* q, const void* k, const void* v, const void* kt,
+                               const void* vt, const void* kd, const void* vd,
+                               const int32_t* parents, const int32_t* lengths, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, int B,
+                               int Hq, int Hkv, int S, int N, int L, int d, float scale,
+                               moda_stream_t stream) {
+  g_msg[0] = 0;
+  moda_status_t s = injected_at_validate();
+  if (s != MODA_OK) return s;
+  s = check_cache_sizes(B, Hq, Hkv, S, N, L, d);
+  if (s != MODA_OK) return s;
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(MODA_ERR_INVALID_ARGUMENT, "scale must be positive and finite");
+  const moda::TreeProblem p{B, Hq, Hkv, S, N, L, d, scale};
+  const size_t need = moda::tree_workspace_bytes(p);
+  const size_t kv = size_t(B) * Hkv * d * 2, nq = size_t(B) * Hq * N;
+  const size_t nd = kv * N * L;
+  const Buf in[9] = {{q, nq * d * 2, 16}, {k, kv * S, 16},  {v, kv * S, 16},
+                     {kt, kv * N, 16},    {vt, kv * N, 16}, {L ? kd : nullptr, nd, 16},
+                     {L ? vd : nullptr, nd, 16}, {parents, size_t(B) * N * 4, 4},
+                     {lengths, size_t(B) * 4, 4}};
+  const Buf outs[3] = {{out, nq * d * 2, 16}, {lse, nq * 4, 16}, {workspace, need, 256}};
+  s = check_buffers(in, outs);
+  if (s != MODA_OK) return s;
+  if (workspace_bytes < need)
+    return fail(MODA_ERR_INVALID_ARGUMENT,
+                "workspace is smaller than moda_tree_decode_workspace_size()");
+  s = injected_at_launch();
+  if (s != MODA_OK) return s;
+  s = check_device();
+  if (s != MODA_OK) return s;
+  moda::EncodeTiledFn enc = get_encoder();
+  if (!enc) return fail(MODA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  const char* why = "";
+  cudaError_t e = moda::launch_tree(p, q, k, v, kt, vt, kd, vd, parents, lengths, out, lse,
+                                    workspace, enc, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) {
     snprintf(g_msg, sizeof(g_msg), "%s: %s", why, cudaGetErrorString(e));
     return MODA_ERR_CUDA;

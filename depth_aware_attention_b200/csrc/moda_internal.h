@@ -83,6 +83,18 @@ cudaError_t launch_decode(const Problem& p, const void* q, const void* k, const 
                           void* workspace, EncodeTiledFn encode, cudaStream_t stream,
                           const char** why);
 
+// Attention of N drafted tokens per sequence over a ragged cache of up to S keys.
+struct TreeProblem {
+  int B, Hq, Hkv, S, N, L, d;
+  float scale;
+};
+size_t tree_workspace_bytes(const TreeProblem& p);
+cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, const void* v,
+                        const void* kt, const void* vt, const void* kd, const void* vd,
+                        const int* parents, const int* lengths, void* out, float* lse,
+                        void* workspace, EncodeTiledFn encode, cudaStream_t stream,
+                        const char** why);
+
 // Fused depth-stream write: K|V = X W^T for B*T tokens, stored into slot `slot` of the
 // [B, Hkv, T, L, d] depth caches.
 struct KvWriteProblem {

@@ -6,3 +6,4 @@
 #include "moda_noalloc.cu"
 #include "moda_decode.cu"
 #include "moda_kvwrite.cu"
+#include "moda_tree.cu"

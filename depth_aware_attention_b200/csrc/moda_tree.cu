@@ -1,0 +1,871 @@
+// moda_tree.cu -- attention of N drafted tokens per sequence over a ragged K/V cache, for
+// B200 (sm_100a).
+//
+// The operator: the MoDA definition (hyper.ai summary of arXiv 2603.15619, section
+// "Mixture-of-Depths Attention (MoDA)") for N new tokens per sequence that form a tree: a
+// token sees every cached key of its sequence, its ancestors among the new tokens and
+// itself, and its own L depth entries, in one joint softmax.  N = 1 is single-token decoding
+// over caches of different lengths.  (The pages describe neither.)
+//
+// What bounds it: each cached K/V byte is needed once and serves the G x N rows of its KV
+// head, so up to 128 rows the work is a stream from HBM and the tensor cores have the FLOPs
+// to spare; from 128 to 256 rows both take about as long.
+//
+//   Tiles.  128 rows = TQ tokens x the G heads of one KV head, token-major, as in the
+//   forward kernel.  With one tile per KV head the two softmax warpgroups take alternate key
+//   blocks, each with its own running maximum, sum and accumulator, merged at the end; with
+//   more tiles they take one tile each of a pair, and every block serves both.
+//   Steps.  An item (sequence, KV head, tile or pair) is a list of 128-key steps: the depth
+//   entries of its tokens (each row sees its own token's), the new tokens (each row sees its
+//   ancestors), the cache blocks.  All run through one TMA ring into the tensor cores.
+//   Split.  The steps of all items are laid in one line and cut into equal shares, one per
+//   CTA, whatever the lengths are: a CTA may end one item and begin the next.  The lengths
+//   are read on the device, so a captured graph follows them.  An item inside one CTA is
+//   written directly; the pieces of a cut item go to the workspace as (maximum, sum, fp32
+//   accumulator) and a second launch joins them, in the order of the steps.
+//   Rows that must not be read as values (behind a cache's length, unused slots, tile rows no
+//   entry fills) are zeroed in shared memory by warp 10 before the tensor cores see them: a
+//   weight of zero times an infinity or a NaN is a NaN.
+//
+// Warp roles (352 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA (lane 0
+// the ring, lane 1 the Q tiles), warp 9 tcgen05 issuer, warp 10 follows the ring and zeroes.
+// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "moda_internal.h"
+#include "moda_packed.cuh"
+#include "sm100.cuh"
+
+namespace moda {
+
+namespace {
+
+constexpr int kTreeThreads = 352;
+constexpr int kTreeCtas = 148;      // one CTA per SM of a B200
+constexpr int kTreeMinShare = 2;    // steps of the smallest share
+constexpr int kTreeRegion = 16384;  // 128 rows x 128 bytes, swizzled
+constexpr float kLog2eTree = 1.4426950408889634f;
+constexpr float kLn2Tree = 0.6931471805599453f;
+constexpr float kTreeRescale = 8.0f;  // log2 units: O is rescaled only past 256x
+
+template <int D, bool kPair>
+struct TreeCfg {
+  static constexpr int kRegions = D / 64;
+  static constexpr int kTile = kRegions * kTreeRegion;
+  static constexpr int kQTiles = kPair ? 2 : 1;
+  static constexpr int kStages = D == 128 ? (kPair ? 5 : 6) : 10;
+  static constexpr int kOffKV = kQTiles * kTile;
+  static constexpr int kOffML = kOffKV + kStages * kTile;  // [2][128] float2
+  static constexpr int kOffBar = kOffML + 2 * 128 * 8;
+  static constexpr int kSmemBytes = kOffBar + 384;
+};
+
+struct TreeArgs {
+  __nv_bfloat16* out;
+  float* lse;
+  float* ws_acc;  // [2 * kTreeCtas][rows][D]
+  float* ws_ml;   // [2 * kTreeCtas][rows][2]: m (log2 units), l
+  const int* parents;
+  const int* lengths;
+  int B, Hq, Hkv, G, N, S, L;
+  int TQ, JC, ND;  // tokens per tile, depth entries per step, depth steps
+  int nit;         // items per sequence: KV heads x tiles (or tile pairs)
+  int nt;          // tiles (or tile pairs) per KV head
+  int rows;        // rows of a workspace slot
+  float scale_log2;
+};
+
+struct TreeBars {
+  uint64_t full[10], empty[10], ready[10];  // ring: landed; released; zeroed where needed
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_final, o_free;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ int tree_length(const TreeArgs& a, int b, bool report = false) {
+  const int n = __ldg(a.lengths + b);
+  if (report && (n < 0 || n > a.S)) atomicOr(&g_error_word, kErrInternal);
+  return min(max(n, 0), a.S);
+}
+// 128-key steps of each item of sequence b
+__device__ __forceinline__ int tree_steps(const TreeArgs& a, int b) {
+  return a.ND + 1 + (tree_length(a, b) + 127) / 128;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Steps of all sequences' items together, and the share of one CTA (all lanes of a warp).
+__device__ __forceinline__ long long tree_share(const TreeArgs& a, long long& total) {
+  const int lane = threadIdx.x & 31;
+  long long n = 0;
+  for (int b = lane; b < a.B; b += 32) n += tree_steps(a, b);
+  total = warp_sum(n) * a.nit;
+  const long long share = (total + kTreeCtas - 1) / kTreeCtas;
+  return share < kTreeMinShare ? kTreeMinShare : share;
+}
+
+// A CTA's walk over its share: piece by piece, each a run of steps of one item.
+struct TreeWalk {
+  long long left;      // steps left behind this piece
+  int b, it;           // sequence and item of it
+  int j0, j1, n, len;  // steps [j0, j1) of n, the sequence's cache length
+  __device__ __forceinline__ void clip(const TreeArgs& a) {
+    len = tree_length(a, b);
+    n = a.ND + 1 + (len + 127) / 128;
+    const long long want = left < n - j0 ? left : n - j0;
+    j1 = j0 + int(want);
+    left -= want;
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
+    if (left <= 0) return false;
+    if (++it == a.nit) {
+      it = 0;
+      ++b;
+    }
+    j0 = 0;
+    clip(a);
+    return true;
+  }
+};
+
+// The first piece of the share [s, s + left) (all lanes of a warp; left > 0).
+__device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, long long s, long long left) {
+  const int lane = threadIdx.x & 31;
+  TreeWalk w;
+  w.left = left;
+  long long before = 0;  // steps of one item of each earlier sequence
+  w.b = 0;
+  w.it = 0;
+  w.j0 = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int mine = b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const bool past = b0 + lane < a.B && (before + incl) * a.nit > s;
+    const uint32_t m = __ballot_sync(0xffffffffu, past);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      const int n = __shfl_sync(0xffffffffu, mine, src);
+      const int at = __shfl_sync(0xffffffffu, incl, src) - n;
+      const long long off = s - (before + at) * a.nit;
+      w.b = b0 + src;
+      w.it = int(off / n);
+      w.j0 = int(off - (long long)w.it * n);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  w.clip(a);
+  return w;
+}
+
+// Bits [lo, hi) of word w of a 128-bit row mask.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+  const int a = min(max(lo - 32 * w, 0), 32), e = min(max(hi - 32 * w, 0), 32);
+  const uint32_t below_e = e == 32 ? 0xffffffffu : (1u << e) - 1u;
+  const uint32_t below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+  return below_e & ~below_a;
+}
+
+// The new tokens that token i sees: itself and its ancestors, as 128 bits.  A parent must
+// come before its child and not be an unused slot; anything else ends the path there and is
+// reported.
+__device__ __forceinline__ void ancestor_bits(const int* par, int i, uint32_t (&vis)[4]) {
+  vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+  auto set = [&](int c) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (c >> 5 == w) vis[w] |= 1u << (c & 31);
+  };
+  set(i);
+  int cur = i, p = __ldg(par + i);
+  if (p == -2) return;
+  while (p >= 0 && p < cur) {
+    const int up = __ldg(par + p);
+    if (up == -2) break;
+    set(p);
+    cur = p;
+    p = up;
+  }
+  if (p != -1) atomicOr(&g_error_word, kErrInternal);
+}
+
+template <int D, bool kPair>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    moda_tree_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmKT,
+                     const __grid_constant__ CUtensorMap tmVT,
+                     const __grid_constant__ CUtensorMap tmKD,
+                     const __grid_constant__ CUtensorMap tmVD, const TreeArgs a) {
+  using Cfg = TreeCfg<D, kPair>;
+  constexpr int NS = Cfg::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // the joining grid may be scheduled now: it waits for this grid's completion itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the swizzled layouts need a 1024-byte aligned base, and there is no room to realign
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_error_word, kErrInternal);
+    return;
+  }
+  const uint32_t s0 = smem_u32(smem);
+  auto sQ = [&](int t) { return s0 + uint32_t(t) * Cfg::kTile; };
+  auto sKV = [&](int s) { return s0 + Cfg::kOffKV + uint32_t(s) * Cfg::kTile; };
+  float2* const ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
+  TreeBars* bars = reinterpret_cast<TreeBars*>(smem + Cfg::kOffBar);
+  static_assert(sizeof(TreeBars) <= 384, "barrier space");
+  volatile int* abort_flag = &bars->abort;
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  long long total;
+  const long long share = tree_share(a, total);
+  const long long first = share * blockIdx.x;
+  if (first >= total) return;
+  const TreeWalk walk0 = tree_first(a, first, min(share, total - first));
+  if (blockIdx.x == 0 && warp == 0)
+    for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar(bars->full[s]), 1);
+      mbar_init(bar(bars->empty[s]), 2);  // the products that read it, and warp 10
+      mbar_init(bar(bars->ready[s]), 1);
+    }
+    mbar_init(bar(bars->q_full), 1);
+    mbar_init(bar(bars->q_empty), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(bars->s_full[t]), 1);
+      mbar_init(bar(bars->p_full[t]), 4);  // one arrival a warp
+    }
+    mbar_init(bar(bars->o_final), 1);
+    mbar_init(bar(bars->o_free), 8);
+    mbar_init(bar(bars->drain), 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  // Q rows past TQ*G never receive TMA data: zero them once
+  if (threadIdx.x < 128 && threadIdx.x >= a.TQ * a.G) {
+    for (int t = 0; t < Cfg::kQTiles * Cfg::kRegions; ++t)
+      for (int c = 0; c < 8; ++c)
+        sts128(s0 + uint32_t(t) * kTreeRegion + threadIdx.x * 128u + c * 16u,
+               make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // Ring entries of a step: keys then values; a depth step of a tile pair has both tiles'
+  // keys, then both tiles' values.
+  auto wide = [&](int j) { return kPair && j < a.ND; };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      int e = 0;
+      TreeWalk w = walk0;
+      bool more = true;
+      while (more && !*abort_flag) {
+        const int g = w.it / a.nt, tile = w.it - g * a.nt;
+        const int bg = w.b * a.Hkv + g;
+        const int tok0 = tile * a.TQ * Cfg::kQTiles;
+        for (int j = w.j0; j < w.j1; ++j) {
+          const int ne = wide(j) ? 4 : 2;
+          bool ok = true;
+          for (int u = 0; u < ne; ++u, ++e) {
+            const int s = e % NS;
+            if (e >= NS && !mbar_wait(bar(bars->empty[s]), ((e / NS) - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const bool values = ne == 4 ? u >= 2 : u == 1;
+            const uint32_t full = bar(bars->full[s]);
+            if (j < a.ND) {
+              mbar_expect_tx(full, uint32_t(Cfg::kRegions) * 128u * a.TQ * a.JC);
+              for (int rg = 0; rg < Cfg::kRegions; ++rg)
+                tma_load_4d(sKV(s) + rg * kTreeRegion, values ? &tmVD : &tmKD, full, rg * 64,
+                            j * a.JC, tok0 + (ne == 4 && (u & 1) ? a.TQ : 0), bg);
+            } else {
+              mbar_expect_tx(full, Cfg::kTile);
+              const bool tree = j == a.ND;
+              const CUtensorMap* map = tree ? (values ? &tmVT : &tmKT) : (values ? &tmV : &tmK);
+              for (int rg = 0; rg < Cfg::kRegions; ++rg)
+                tma_load_3d(sKV(s) + rg * kTreeRegion, map, full, rg * 64,
+                            tree ? 0 : (j - a.ND - 1) * 128, bg);
+            }
+          }
+          if (!ok) break;
+        }
+        more = w.next(a);
+      }
+      if (*abort_flag)  // abort path: what was issued still lands; wait for it before exit
+        for (int i = e > NS ? e - NS : 0; i < e; ++i)
+          mbar_wait_drain(bar(bars->full[i % NS]), (i / NS) & 1);
+    } else if (lane == 1) {
+      TreeWalk w = walk0;
+      int pc = 0;  // piece
+      bool more = true;
+      for (; more; ++pc, more = w.next(a)) {
+        if (pc > 0 && !mbar_wait(bar(bars->q_empty), (pc - 1) & 1, abort_flag)) break;
+        const int g = w.it / a.nt, tile = w.it - g * a.nt;
+        mbar_expect_tx(bar(bars->q_full),
+                       uint32_t(Cfg::kQTiles * Cfg::kRegions) * 128u * a.G * a.TQ);
+        for (int t = 0; t < Cfg::kQTiles; ++t)
+          for (int rg = 0; rg < Cfg::kRegions; ++rg)
+            tma_load_4d(sQ(t) + rg * kTreeRegion, &tmQ, bar(bars->q_full), rg * 64, 0,
+                        (tile * Cfg::kQTiles + t) * a.TQ, w.b * a.Hkv + g);
+      }
+      if (*abort_flag && pc > 0) mbar_wait_drain(bar(bars->q_full), (pc - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tcgen05 issuer
+    // Units: (step) with the warpgroup alternating, or (step, tile) for a pair.  Order:
+    // S(0) S(1) { PV(u) S(u+2) }: while one warpgroup turns its S into P the tensor cores
+    // work for the other.  S(u+2) overwrites P(u), which PV(u), issued before it, has read.
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idesc_o = make_idesc_bf16(128, D, 0, 1);
+      struct Cursor {
+        TreeWalk w;
+        int j, half, e, pc, u;  // step, tile of the pair, ring entry, piece, unit
+        bool live;
+      };
+      Cursor cs{walk0, walk0.j0, 0, 0, 0, 0, true};
+      Cursor cp = cs;
+      auto advance = [&](Cursor& c) {
+        ++c.u;
+        if (kPair && c.half == 0) {
+          c.half = 1;
+          return;
+        }
+        c.half = 0;
+        c.e += wide(c.j) ? 4 : 2;
+        if (++c.j == c.w.j1) {
+          c.live = c.w.next(a);
+          c.j = c.w.j0;
+          ++c.pc;
+        }
+      };
+      auto issue_s = [&](Cursor& c) {
+        const int wg = c.u & 1;
+        const bool two = wide(c.j);
+        const int e = c.e + (two ? c.half : 0);
+        if (c.j == c.w.j0 && c.half == 0) mbar_wait(bar(bars->q_full), c.pc & 1, abort_flag);
+        mbar_wait(bar(bars->full[e % NS]), (e / NS) & 1, abort_flag);
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks / 4) * kTreeRegion + (ks % 4) * 32;
+          mma_ss(tmem + wg * 128, make_sdesc_sw128(sQ(kPair ? c.half : 0) + off, 16, 1024),
+                 make_sdesc_sw128(sKV(e % NS) + off, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(bars->s_full[wg]));
+        if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
+        if (c.j == c.w.j1 - 1 && (!kPair || c.half == 1)) tc_commit(bar(bars->q_empty));
+        advance(c);
+      };
+      auto issue_pv = [&](Cursor& c) {
+        const int wg = c.u & 1;
+        const bool two = wide(c.j);
+        const int e = c.e + (two ? 2 + c.half : 1);
+        mbar_wait(bar(bars->ready[e % NS]), (e / NS) & 1, abort_flag);
+        mbar_wait(bar(bars->p_full[wg]), (c.u >> 1) & 1, abort_flag);
+        // the accumulators of the piece before have been read
+        if (c.pc > 0 && c.j == c.w.j0 && c.half == 0)
+          mbar_wait(bar(bars->o_free), (c.pc - 1) & 1, abort_flag);
+        tc_fence_after();
+        // this warpgroup's first product of the piece overwrites its accumulator
+        const bool fresh = kPair ? c.j == c.w.j0 : c.j - c.w.j0 < 2;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + ks * 8,
+                 make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
+                 (ks > 0 || !fresh) ? 1u : 0u);
+        if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
+        if (c.j == c.w.j1 - 1 && (!kPair || c.half == 1)) tc_commit(bar(bars->o_final));
+        advance(c);
+      };
+      issue_s(cs);
+      if (cs.live) issue_s(cs);
+      while (cp.live && !*abort_flag) {
+        issue_pv(cp);
+        if (cs.live) issue_s(cs);
+      }
+      if (*abort_flag) {
+        tc_commit(bar(bars->drain));
+        mbar_wait_drain(bar(bars->drain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ rows that are no values
+    // zeroes the `each` rows of every unused slot among the new tokens [t0, t1)
+    auto zero_unused = [&](uint32_t tile, const int* par, int t0, int t1, int each) {
+      for (int t = t0; t < t1; t += 32) {
+        uint32_t unused =
+            __ballot_sync(0xffffffffu, t + lane < t1 && __ldg(par + t + lane) == -2);
+        for (; unused; unused &= unused - 1) {
+          const int i = t - t0 + __ffs(unused) - 1;
+          zero_tile_rows(tile, Cfg::kRegions, i * each, (i + 1) * each);
+        }
+      }
+    };
+    int e = 0;
+    TreeWalk w = walk0;
+    bool more = true, stop = false;
+    while (more && !stop) {
+      const int tile = w.it % a.nt;
+      const int tok0 = tile * a.TQ * Cfg::kQTiles;
+      const int* par = a.parents + (long long)w.b * a.N;
+      for (int j = w.j0; j < w.j1 && !stop; ++j) {
+        const int ne = wide(j) ? 4 : 2;
+        for (int u = 0; u < ne; ++u, ++e) {
+          const int s = e % NS;
+          stop = !__all_sync(0xffffffffu, mbar_wait(bar(bars->full[s]), (e / NS) & 1, abort_flag));
+          if (stop) break;
+          if (ne == 4 ? u >= 2 : u == 1) {
+            if (j < a.ND) {
+              // rows that no entry fills, and the entries of unused slots
+              const int t0 = tok0 + (ne == 4 && (u & 1) ? a.TQ : 0);
+              zero_tile_rows(sKV(s), Cfg::kRegions, a.TQ * a.JC, 128);
+              zero_unused(sKV(s), par, t0, min(t0 + a.TQ, a.N), a.JC);
+            } else if (j == a.ND) {
+              zero_unused(sKV(s), par, 0, a.N, 1);
+            } else {
+              const int inside = w.len - (j - a.ND - 1) * 128;
+              if (inside < 128) zero_tile_rows(sKV(s), Cfg::kRegions, inside, 128);
+            }
+          }
+          publish_rows(bar(bars->ready[s]));
+          if (lane == 0) mbar_arrive(bar(bars->empty[s]));
+        }
+      }
+      more = w.next(a);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    const int wg = warp >> 2;
+    const int r = threadIdx.x & 127;  // tile row
+    const int tok = r / a.G, hl = r - tok * a.G;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + wg * 128;
+    const uint32_t tO = tmem + lane_base + 256 + wg * D;
+    TreeWalk w = walk0;
+    int u = 0;  // unit
+    int pc = 0;
+    bool more = true;
+    // (no early way out: the warpgroups meet at named barriers; once a wait has failed every
+    // later one returns at once)
+    for (; more; ++pc) {
+      const int g = w.it / a.nt, tile = w.it - g * a.nt;
+      const int t0 = (tile * Cfg::kQTiles + (kPair ? wg : 0)) * a.TQ;
+      const int ti = t0 + tok;  // this row's new token
+      const int* par = a.parents + (long long)w.b * a.N;
+      const bool valid = tok < a.TQ && ti < a.N;
+      // warps without a row in the tile only keep the barriers in step
+      const bool active = (warp & 3) * 32 < min(a.TQ, a.N - t0) * a.G;
+      float m = -INFINITY, l = 0.f;
+      bool has_o = false;
+      for (int j = w.j0; j < w.j1; ++j) {
+        if (!kPair && ((u + j - w.j0) & 1) != wg) continue;
+        const int unit = kPair ? u + 2 * (j - w.j0) + wg : u + j - w.j0;
+        mbar_wait(bar(bars->s_full[wg]), (unit >> 1) & 1, abort_flag);
+        tc_fence_after();
+        if (active) {
+          uint32_t s[128];
+          tmem_ld32(tS + 0, &s[0]);
+          tmem_ld32(tS + 32, &s[32]);
+          tmem_ld32(tS + 64, &s[64]);
+          tmem_ld32(tS + 96, &s[96]);
+          uint32_t vis[4];
+          bool masked = true;
+          if (j < a.ND) {
+            const int lo = tok * a.JC, nv = min(a.JC, a.L - j * a.JC);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) vis[q] = valid ? range_bits(lo, lo + nv, q) : 0u;
+          } else if (j == a.ND) {
+            if (valid)
+              ancestor_bits(par, ti, vis);
+            else
+              vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+          } else {
+            const int inside = w.len - (j - a.ND - 1) * 128;
+            masked = inside < 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) vis[q] = range_bits(0, inside, q);
+          }
+          tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+          }
+          float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
+          const float m_cand = fmaxf(m, fmaxf(mx, mx1) * a.scale_log2);
+          const bool grow = m_cand > m + kTreeRescale;
+          const float m_new = grow ? m_cand : m;
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+          const float alpha = ex2(m - m_use);
+          // every product of this warpgroup so far was issued before its S and has finished
+          if (__any_sync(0xffffffffu, grow && has_o)) {
+            const float f = grow ? alpha : 1.f;
+#pragma unroll 1
+            for (int cc = 0; cc < D / 16; ++cc) {
+              uint32_t o[16];
+              tmem_ld16(tO + cc * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(tO + cc * 16, o);
+            }
+          }
+          const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+          const float2 nm2 = make_float2(-m_use, -m_use);
+          float2 ps = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // P enters its product as bf16 (the products' operand type); l sums it unrounded
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float2 x = ffma2(make_float2(__uint_as_float(s[half * 64 + c]),
+                                                 __uint_as_float(s[half * 64 + c + 1])),
+                                     sl2, nm2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              ps = fadd2(ps, p);
+              pk[c / 2] = pack_bf16x2(p.x, p.y);
+            }
+            tmem_st32(tS + half * 32, pk);
+          }
+          l = l * alpha + (ps.x + ps.y);
+          m = m_new;
+          has_o = true;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->p_full[wg]));
+      }
+      // ---- the piece's end
+      const int units = (w.j1 - w.j0) * Cfg::kQTiles;
+      mbar_wait(bar(bars->o_final), pc & 1, abort_flag);
+      tc_fence_after();
+      const bool whole = w.j0 == 0 && w.j1 == w.n;
+      float m_all = m, l_all = l, f0 = 1.f, f1 = 0.f;
+      constexpr int kCols = kPair ? D : D / 2;  // columns this thread writes
+      const int col0 = kPair ? 0 : wg * kCols;
+      if constexpr (!kPair) {
+        ml[wg * 128 + r] = make_float2(m, l);
+        named_bar_sync(1, 256);
+        const float2 x = ml[r], y = ml[128 + r];
+        named_bar_sync(1, 256);  // (the next piece writes them again)
+        m_all = fmaxf(x.x, y.x);
+        const float mu = m_all == -INFINITY ? 0.f : m_all;
+        f0 = ex2(x.x - mu);
+        f1 = ex2(y.x - mu);
+        l_all = x.y * f0 + y.y * f1;
+      }
+      // which accumulators hold anything: with a single unit only its warpgroup's does
+      const bool use0 = kPair || units > 1 || (u & 1) == 0;
+      const bool use1 = !kPair && (units > 1 || (u & 1) == 1);
+      if (active) {
+        const bool dead = valid && __ldg(par + ti) == -2;  // unused slot: zeros, -inf
+        // (l = 0 only for a row that saw nothing)
+        const float inv = whole ? ((dead || l_all == 0.f) ? 0.f : 1.f / l_all) : 1.f;
+        const long long row =
+            ((long long)w.b * a.Hq + g * a.G + hl) * a.N + (valid ? ti : 0);
+        // a cut item's first piece in a CTA's share has the share's first slot
+        const int slot = 2 * int(blockIdx.x) + (pc > 0 ? 1 : 0);
+        const long long wrow = (long long)slot * a.rows + (kPair ? wg * a.TQ * a.G : 0) + r;
+#pragma unroll
+        for (int cc = 0; cc < kCols / 32; ++cc) {
+          uint32_t o[32], o1[32];
+          if constexpr (kPair) {
+            tmem_ld32(tO + cc * 32, o);
+          } else {
+            tmem_ld32(tmem + lane_base + 256 + col0 + cc * 32, o);
+            tmem_ld32(tmem + lane_base + 256 + D + col0 + cc * 32, o1);
+          }
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if constexpr (kPair) {
+              v[i] = __uint_as_float(o[i]);
+            } else {
+              v[i] = (use0 ? f0 * __uint_as_float(o[i]) : 0.f) +
+                     (use1 ? f1 * __uint_as_float(o1[i]) : 0.f);
+            }
+          }
+          if (valid) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + col0 + cc * 32);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = inv == 0.f ? 0.f : v[q * 8 + i];
+                dst[q] = pack8(x, inv);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.ws_acc + wrow * D + col0 + cc * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+          }
+        }
+        if (valid && (kPair || wg == 0)) {
+          if (whole)
+            a.lse[row] = (dead || l_all == 0.f) ? -INFINITY : (m_all + __log2f(l_all)) * kLn2Tree;
+          else
+            *reinterpret_cast<float2*>(a.ws_ml + wrow * 2) = make_float2(m_all, l_all);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars->o_free));
+      u += units;
+      more = w.next(a);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the items that were cut: one warp per row (sequence, head, token), a
+// lane for every 32nd group of four columns.  Rows of items inside one CTA's share were
+// written by it.
+template <int D>
+__global__ void __launch_bounds__(256) moda_tree_join_kernel(const TreeArgs a, int qtiles) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (long long)a.B * a.Hq * a.N) return;
+  long long total;
+  const long long share = tree_share(a, total);
+  const int i = int(row % a.N);
+  const int h = int(row / a.N % a.Hq), b = int(row / a.N / a.Hq);
+  const int g = h / a.G, hl = h - g * a.G;
+  long long before = 0;
+  for (int x = lane; x < b; x += 32) before += tree_steps(a, x);
+  before = warp_sum(before) * a.nit;
+  const int n = tree_steps(a, b);
+  const int tile = i / a.TQ, item = g * a.nt + tile / qtiles;
+  const long long s = before + (long long)item * n;
+  const int c0 = int(s / share), c1 = int((s + n - 1) / share);
+  // the pieces' grid: wait for its completion
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;
+  const int r = (tile % qtiles) * a.TQ * a.G + (i - tile * a.TQ) * a.G + hl;
+  auto slot_row = [&](int c) {
+    return (long long)(2 * c + (s > c * share ? 1 : 0)) * a.rows + r;
+  };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ws_ml[slot_row(c) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float Mu = M == -INFINITY ? 0.f : M;
+  constexpr int kV = D / 32;  // columns per lane
+  float acc[kV], den = 0.f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const long long wr = slot_row(c);
+    const float2 x = *reinterpret_cast<const float2*>(a.ws_ml + wr * 2);
+    const float f = ex2(x.x - Mu);
+    den = fmaf(f, x.y, den);
+    const float* p = a.ws_acc + wr * D + lane * kV;
+    // (a piece in which the row saw nothing has weight zero)
+    if constexpr (kV == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p);
+      acc[0] = fmaf(f, y.x, acc[0]);
+      acc[1] = fmaf(f, y.y, acc[1]);
+      acc[2] = fmaf(f, y.z, acc[2]);
+      acc[3] = fmaf(f, y.w, acc[3]);
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(p);
+      acc[0] = fmaf(f, y.x, acc[0]);
+      acc[1] = fmaf(f, y.y, acc[1]);
+    }
+  }
+  const bool none = den == 0.f || __ldg(a.parents + (long long)b * a.N + i) == -2;
+  const float inv = none ? 0.f : 1.f / den;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc[v] = none ? 0.f : acc[v] * inv;
+  __nv_bfloat16* dst = a.out + row * D + lane * kV;
+  if constexpr (kV == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+  if (lane == 0) a.lse[row] = none ? -INFINITY : (Mu + __log2f(den)) * kLn2Tree;
+}
+
+struct TreeGeom {
+  int TQ, JC, ND, tiles, nt, rows;
+  bool pair;
+};
+TreeGeom tree_geom(int N, int G, int L) {
+  TreeGeom t;
+  t.TQ = min(N, 128 / G);
+  t.JC = 128 / t.TQ;
+  t.ND = (L + t.JC - 1) / t.JC;
+  t.tiles = (N + t.TQ - 1) / t.TQ;
+  t.pair = t.tiles > 1;
+  t.nt = t.pair ? (t.tiles + 1) / 2 : 1;
+  t.rows = t.TQ * G * (t.pair ? 2 : 1);
+  return t;
+}
+
+template <int D, bool kPair>
+cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeArgs& a,
+                          const void* q, const void* k, const void* v, const void* kt,
+                          const void* vt, const void* kd, const void* vd, EncodeTiledFn encode,
+                          cudaStream_t stream, const char** why) {
+  using Cfg = TreeCfg<D, kPair>;
+  const cuuint64_t E = 2, BG = cuuint64_t(p.B) * p.Hkv;
+  auto map = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                 const cuuint64_t* str, const cuuint32_t* box) {
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, str,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  CUtensorMap mQ, mK, mV, mKT, mVT, mKD, mVD;
+  bool ok;
+  {
+    const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(a.G), cuuint64_t(p.N), BG};
+    const cuuint64_t str[3] = {cuuint64_t(p.N) * D * E, cuuint64_t(D) * E,
+                               cuuint64_t(a.G) * p.N * D * E};
+    const cuuint32_t box[4] = {64, cuuint32_t(a.G), cuuint32_t(tg.TQ), 1};
+    ok = map(&mQ, q, 4, dims, str, box);
+  }
+  auto keys = [&](CUtensorMap* m, const void* base, int rows) {
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(rows), BG};
+    const cuuint64_t str[2] = {cuuint64_t(D) * E, cuuint64_t(rows) * D * E};
+    const cuuint32_t box[3] = {64, 128, 1};
+    return map(m, base, 3, dims, str, box);
+  };
+  ok = ok && keys(&mK, k, p.S) && keys(&mV, v, p.S) && keys(&mKT, kt, p.N) && keys(&mVT, vt, p.N);
+  mKD = mK;  // never loaded when L == 0
+  mVD = mV;
+  if (p.L > 0) {
+    const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(p.L), cuuint64_t(p.N), BG};
+    const cuuint64_t str[3] = {cuuint64_t(D) * E, cuuint64_t(p.L) * D * E,
+                               cuuint64_t(p.N) * p.L * D * E};
+    const cuuint32_t box[4] = {64, cuuint32_t(tg.JC), cuuint32_t(tg.TQ), 1};
+    ok = ok && map(&mKD, kd, 4, dims, str, box) && map(&mVD, vd, 4, dims, str, box);
+  }
+  if (!ok) {
+    *why = "cuTensorMapEncodeTiled failed for the tree attention's tensors";
+    return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(moda_tree_kernel<D, kPair>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg::kSmemBytes);
+  if (e != cudaSuccess) {
+    *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+    return e;
+  }
+  moda_tree_kernel<D, kPair><<<kTreeCtas, kTreeThreads, Cfg::kSmemBytes, stream>>>(
+      mQ, mK, mV, mKT, mVT, mKD, mVD, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    *why = "tree attention launch failed";
+    return e;
+  }
+  // programmatic dependent launch: see the decode's combine step
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(((long long)p.B * p.Hq * p.N + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, moda_tree_join_kernel<D>, a, kPair ? 2 : 1);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) *why = "tree attention join launch failed";
+  return e;
+}
+
+}  // namespace
+
+size_t tree_workspace_bytes(const TreeProblem& p) {
+  const TreeGeom t = tree_geom(p.N, p.Hq / p.Hkv, p.L);
+  return size_t(2 * kTreeCtas) * t.rows * (p.d + 2) * 4;
+}
+
+cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, const void* v,
+                        const void* kt, const void* vt, const void* kd, const void* vd,
+                        const int* parents, const int* lengths, void* out, float* lse,
+                        void* workspace, EncodeTiledFn encode, cudaStream_t stream,
+                        const char** why) {
+  const int G = p.Hq / p.Hkv;
+  const TreeGeom t = tree_geom(p.N, G, p.L);
+  TreeArgs a;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.ws_acc = static_cast<float*>(workspace);
+  a.ws_ml = a.ws_acc + size_t(2 * kTreeCtas) * t.rows * p.d;
+  a.parents = parents;
+  a.lengths = lengths;
+  a.B = p.B;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = G;
+  a.N = p.N;
+  a.S = p.S;
+  a.L = p.L;
+  a.TQ = t.TQ;
+  a.JC = t.JC;
+  a.ND = t.ND;
+  a.nt = t.nt;
+  a.nit = p.Hkv * t.nt;
+  a.rows = t.rows;
+  a.scale_log2 = p.scale * kLog2eTree;
+  if (p.d == 128)
+    return t.pair ? launch_tree_d<128, true>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why)
+                  : launch_tree_d<128, false>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
+                                              why);
+  return t.pair ? launch_tree_d<64, true>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why)
+                : launch_tree_d<64, false>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why);
+}
+
+}  // namespace moda

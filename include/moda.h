@@ -191,6 +191,40 @@ moda_status_t moda_decode(const void *q, const void *k, const void *v, const voi
                           float scale, moda_stream_t stream);
 
 /*
+ * Attention of N drafted tokens per sequence over a ragged K/V cache: sequence b has
+ * lengths[b] cached keys (of room for S) and N new tokens that form a tree.  Token i sees
+ * every cached key of its sequence, its ancestors among the new tokens and itself, and its
+ * own L depth keys, in one joint softmax (hyper.ai summary of arXiv 2603.15619, section
+ * "Mixture-of-Depths Attention (MoDA)"; the pages describe no decoding).  N = 1 with parent
+ * -1 is single-token decoding over caches of different lengths.
+ *   q, out: bf16 [B][Hq][N][d]     k, v: bf16 [B][Hkv][S][d] (the cache, new tokens NOT in it)
+ *   kt, vt: bf16 [B][Hkv][N][d]    the new tokens' own keys and values
+ *   kd, vd: bf16 [B][Hkv][N][L][d] their depth entries (NULL iff L == 0)
+ *   lse:    fp32 [B][Hq][N]
+ *   parents: int32 [B][N], device: the parent of token i, a token before it; -1: token i
+ *            follows the cache directly; -2: slot i is unused.
+ *   lengths: int32 [B], device, 0 <= lengths[b] <= S.
+ * A line of drafts is parents = -1, 0, 1, ...  An unused slot's row gets out = 0 and lse =
+ * -inf, whatever its inputs hold, and nothing sees its key.  Cache rows from lengths[b] on are
+ * not read into any result, whatever bits they hold.  Values in use must be finite.
+ * Entries of parents and lengths that break the rules above are known on the device alone:
+ * they set bit 2 of the device error word (moda_check_device_errors() returns
+ * MODA_ERR_INTERNAL); the path of a bad parent ends at its child, a bad length is clamped.
+ * Both are read when the kernel runs, so a captured graph follows them.
+ * workspace: >= moda_tree_decode_workspace_size(...) bytes, 256-byte aligned, owned by the
+ * caller, contents irrelevant; calls that may overlap on the GPU need one each.
+ * N <= 128, Hq / Hkv <= 64, d in {64, 128} (MODA_ERR_UNSUPPORTED otherwise); scale > 0; other
+ * rules as moda_forward.  Two launches; the result is the same bits on every run.
+ */
+size_t moda_tree_decode_workspace_size(int B, int Hq, int Hkv, int S, int N, int L, int d);
+moda_status_t moda_tree_decode(const void *q, const void *k, const void *v, const void *kt,
+                               const void *vt, const void *kd, const void *vd,
+                               const int32_t *parents, const int32_t *lengths, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes, int B,
+                               int Hq, int Hkv, int S, int N, int L, int d, float scale,
+                               moda_stream_t stream);
+
+/*
  * Fused depth-stream write: the projection that produces a sublayer's depth key/value
  * pair, with the depth cache as its output (hyper.ai summary of arXiv 2603.15619,
  * section "Hardware-efficient implementation": every layer appends its K/V to the
