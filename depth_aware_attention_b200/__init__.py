@@ -32,7 +32,8 @@ BACKWARD_LAUNCHES = 3
 EXPORTED = ("moda_forward", "moda_forward_depth_path", "moda_depth_attention_forward",
             "moda_depth_attention_backward", "moda_decode", "moda_decode_workspace_size",
             "moda_depth_kv_write", "moda_forward_packed", "moda_backward_packed",
-            "moda_tree_decode", "moda_tree_decode_workspace_size",
+            "moda_tree_decode", "moda_tree_decode_workspace_size", "moda_cache_score",
+            "moda_cache_evict",
             "moda_backward", "moda_backward_workspace_size",
             "moda_backward_stages", "moda_backward_noalloc", "moda_check_device_errors",
             "moda_test_set_device_fault", "moda_test_exp2_fma", "moda_status_string",
@@ -82,6 +83,10 @@ def _load():
     lib.moda_tree_decode_workspace_size.restype = S
     lib.moda_tree_decode.argtypes = [P] * 12 + [S] + [I] * 7 + [F, P]
     lib.moda_tree_decode.restype = I
+    lib.moda_cache_score.argtypes = [P] * 6 + [I] * 6 + [F, P]
+    lib.moda_cache_score.restype = I
+    lib.moda_cache_evict.argtypes = [P] * 9 + [I] * 7 + [P]
+    lib.moda_cache_evict.restype = I
     lib.moda_test_set_device_fault.argtypes = [I, ctypes.c_uint64]
     lib.moda_test_set_device_fault.restype = I
     lib.moda_test_exp2_fma.argtypes = [P, P, I, P]
@@ -199,6 +204,19 @@ def moda_tree_decode(q, k, v, kt, vt, kd, vd, parents, lengths, out, lse, worksp
     """Direct call of moda_tree_decode with raw pointers (ints) and a stream handle."""
     return lib.moda_tree_decode(q, k, v, kt, vt, kd, vd, parents, lengths, out, lse, workspace,
                                 workspace_bytes, B, Hq, Hkv, S, N, L, d, float(scale), stream)
+
+
+def moda_cache_score(q, k, lse, lengths, score, score_out, B, Hq, Hkv, S, N, d, scale, stream):
+    """Direct call of moda_cache_score with raw pointers (ints) and a stream handle."""
+    return lib.moda_cache_score(q, k, lse, lengths, score, score_out, B, Hq, Hkv, S, N, d,
+                                float(scale), stream)
+
+
+def moda_cache_evict(k, v, score, lengths, k_out, v_out, score_out, index, lengths_out, B, Hkv,
+                     S, keep, sinks, recent, d, stream):
+    """Direct call of moda_cache_evict with raw pointers (ints) and a stream handle."""
+    return lib.moda_cache_evict(k, v, score, lengths, k_out, v_out, score_out, index,
+                                lengths_out, B, Hkv, S, keep, sinks, recent, d, stream)
 
 
 def moda_backward_workspace_size(B, Hq, Hkv, T, L, d):
@@ -651,3 +669,63 @@ def tree_decode(q, k, v, kt, vt, parents, lengths, kd=None, vd=None, scale=None,
           _at(vt), _at(kd) if L else None, _at(vd) if L else None, _at(parents), _at(lengths),
           _at(out), _at(lse), _at(workspace), _nbytes(workspace), B, Hq, Hkv, S, N, L, d, scale)
     return out, lse
+
+
+def cache_score(q, k, lse, lengths, score, scale=None, out=None):
+    """Adds to each cached key's score the attention weight that the newest N tokens of its
+    sequence give it, summed over the heads of the KV group, on the current CUDA stream.
+    Returns the new scores [B,Hkv,S]: a new tensor, or ``out``, which may be ``score`` itself.
+
+    q [B,Hq,N,d] and lse [B,Hq,N] (as attention returned it) of the tokens at positions
+    lengths[b]-N .. lengths[b]-1 of the cache k [B,Hkv,S,d]; score fp32 [B,Hkv,S].
+    """
+    import torch
+    _ndim("q", q, 4)
+    _ndim("k", k, 4)
+    B, Hq, N, d = q.shape
+    Hkv, S = k.shape[1], k.shape[2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(score)
+    f32 = torch.float32
+    _checked(q.device, [("q", q, (B, Hq, N, d), torch.bfloat16),
+                        ("k", k, (B, Hkv, S, d), torch.bfloat16), ("lse", lse, (B, Hq, N), f32),
+                        ("lengths", lengths, (B,), torch.int32),
+                        ("score", score, (B, Hkv, S), f32), ("out", out, (B, Hkv, S), f32)])
+    _call(lib.moda_cache_score, "moda_cache_score", q.device, _at(q), _at(k), _at(lse),
+          _at(lengths), _at(score), _at(out), B, Hq, Hkv, S, N, d, scale)
+    return out
+
+
+def cache_evict(k, v, score, lengths, keep, sinks=0, recent=0, k_out=None, v_out=None,
+                score_out=None, index=None, lengths_out=None):
+    """Cuts every KV head's cache down to its min(lengths[b], keep) best entries, in their old
+    order: the first ``sinks``, the last ``recent`` and the highest scores of the rest, ties to
+    the lowest position.  Returns dict(k_out, v_out [B,Hkv,keep,d], score_out [B,Hkv,keep],
+    index [B,Hkv,keep] (old positions, int32), lengths_out [B]); rows from lengths_out[b] on
+    are not written.  k/v [B,Hkv,S,d], score fp32 [B,Hkv,S], lengths int32 [B].
+    """
+    import torch
+    _ndim("k", k, 4)
+    B, Hkv, S, d = k.shape
+    keep, sinks, recent = int(keep), int(sinks), int(recent)
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    new = lambda t, shape, dtype: (torch.empty(shape, device=k.device, dtype=dtype)  # noqa: E731
+                                   if t is None else t)
+    r = dict(k_out=new(k_out, (B, Hkv, keep, d), bf), v_out=new(v_out, (B, Hkv, keep, d), bf),
+             score_out=new(score_out, (B, Hkv, keep), f32),
+             index=new(index, (B, Hkv, keep), i32), lengths_out=new(lengths_out, (B,), i32))
+    _checked(k.device, [("k", k, (B, Hkv, S, d), bf), ("v", v, (B, Hkv, S, d), bf),
+                        ("score", score, (B, Hkv, S), f32), ("lengths", lengths, (B,), i32),
+                        ("k_out", r["k_out"], (B, Hkv, keep, d), bf),
+                        ("v_out", r["v_out"], (B, Hkv, keep, d), bf),
+                        ("score_out", r["score_out"], (B, Hkv, keep), f32),
+                        ("index", r["index"], (B, Hkv, keep), i32),
+                        ("lengths_out", r["lengths_out"], (B,), i32)])
+    _call(lib.moda_cache_evict, "moda_cache_evict", k.device, _at(k), _at(v), _at(score),
+          _at(lengths), _at(r["k_out"]), _at(r["v_out"]), _at(r["score_out"]), _at(r["index"]),
+          _at(r["lengths_out"]), B, Hkv, S, keep, sinks, recent, d)
+    return r

@@ -406,6 +406,82 @@ moda_status_t moda_tree_decode(const void* q, const void* k, const void* v, cons
   return MODA_OK;
 }
 
+moda_status_t moda_cache_score(const void* q, const void* k, const float* lse,
+                               const int32_t* lengths, const float* score, float* score_out,
+                               int B, int Hq, int Hkv, int S, int N, int d, float scale,
+                               moda_stream_t stream) {
+  g_msg[0] = 0;
+  moda_status_t s = injected_at_validate();
+  if (s != MODA_OK) return s;
+  s = check_cache_sizes(B, Hq, Hkv, S, N, 0, d);
+  if (s != MODA_OK) return s;
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(MODA_ERR_INVALID_ARGUMENT, "scale must be positive and finite");
+  const size_t kv = size_t(B) * Hkv * S, nq = size_t(B) * Hq * N;
+  // score_out may be score itself (the sums are added in place), but not overlap it otherwise
+  const Buf in[5] = {{q, nq * d * 2, 16}, {k, kv * d * 2, 16}, {lse, nq * 4, 4},
+                     {lengths, size_t(B) * 4, 4},
+                     {score, score == score_out ? 0 : kv * 4, 4}};
+  const Buf outs[1] = {{score_out, kv * 4, 4}};
+  s = check_buffers(in, outs);
+  if (s != MODA_OK) return s;
+  s = injected_at_launch();
+  if (s != MODA_OK) return s;
+  s = check_device();
+  if (s != MODA_OK) return s;
+  moda::EncodeTiledFn enc = get_encoder();
+  if (!enc) return fail(MODA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  const char* why = "";
+  cudaError_t e =
+      moda::launch_score(moda::ScoreProblem{B, Hq, Hkv, S, N, d, scale}, q, k, lse, lengths, score,
+                         score_out, enc, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) {
+    snprintf(g_msg, sizeof(g_msg), "%s: %s", why, cudaGetErrorString(e));
+    return MODA_ERR_CUDA;
+  }
+  return MODA_OK;
+}
+
+moda_status_t moda_cache_evict(const void* k, const void* v, const float* score,
+                               const int32_t* lengths, void* k_out, void* v_out,
+                               float* score_out, int32_t* index, int32_t* lengths_out, int B,
+                               int Hkv, int S, int keep, int sinks, int recent, int d,
+                               moda_stream_t stream) {
+  g_msg[0] = 0;
+  moda_status_t s = injected_at_validate();
+  if (s != MODA_OK) return s;
+  s = check_cache_sizes(B, Hkv, Hkv, S, 1, 0, d);
+  if (s != MODA_OK) return s;
+  if (keep < 1 || sinks < 0 || recent < 0 || 1LL * sinks + recent > keep)
+    return fail(MODA_ERR_INVALID_ARGUMENT,
+                "keep >= 1, sinks >= 0, recent >= 0 and sinks + recent <= keep must hold");
+  // the selection's grid is 8 CTAs, the copy's at most one block per 64 kept rows, a KV head
+  const long long most = keep < S ? keep : S;
+  if (1LL * B * Hkv * (most / 64 + 8) > 0x7fffffffll)
+    return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");
+  const size_t bg = size_t(B) * Hkv, row = size_t(d) * 2;
+  const Buf in[4] = {{k, bg * S * row, 16}, {v, bg * S * row, 16}, {score, bg * S * 4, 4},
+                     {lengths, size_t(B) * 4, 4}};
+  const Buf outs[5] = {{k_out, bg * keep * row, 16}, {v_out, bg * keep * row, 16},
+                       {score_out, bg * keep * 4, 4}, {index, bg * keep * 4, 4},
+                       {lengths_out, size_t(B) * 4, 4}};
+  s = check_buffers(in, outs);
+  if (s != MODA_OK) return s;
+  s = injected_at_launch();
+  if (s != MODA_OK) return s;
+  s = check_device();
+  if (s != MODA_OK) return s;
+  const char* why = "";
+  cudaError_t e = moda::launch_evict(moda::EvictProblem{B, Hkv, S, keep, sinks, recent, d}, k, v,
+                                     score, lengths, k_out, v_out, score_out, index, lengths_out,
+                                     static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) {
+    snprintf(g_msg, sizeof(g_msg), "%s: %s", why, cudaGetErrorString(e));
+    return MODA_ERR_CUDA;
+  }
+  return MODA_OK;
+}
+
 moda_status_t moda_depth_kv_write(const void* x, const void* w, void* kd, void* vd, int B,
                                   int T, int hidden, int Hkv, int d, int L, int slot,
                                   moda_stream_t stream) {

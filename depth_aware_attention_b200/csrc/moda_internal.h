@@ -95,6 +95,23 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
                         void* workspace, EncodeTiledFn encode, cudaStream_t stream,
                         const char** why);
 
+// The weight that the newest N queries of each sequence give to its cached keys.
+struct ScoreProblem {
+  int B, Hq, Hkv, S, N, d;
+  float scale;
+};
+cudaError_t launch_score(const ScoreProblem& p, const void* q, const void* k, const float* lse,
+                         const int* lengths, const float* score, float* score_out,
+                         EncodeTiledFn encode, cudaStream_t stream, const char** why);
+
+// A cache cut down to its `keep` best entries per KV head.
+struct EvictProblem {
+  int B, Hkv, S, keep, sinks, recent, d;
+};
+cudaError_t launch_evict(const EvictProblem& p, const void* k, const void* v, const float* score,
+                         const int* lengths, void* k_out, void* v_out, float* score_out,
+                         int* index, int* lengths_out, cudaStream_t stream, const char** why);
+
 // Fused depth-stream write: K|V = X W^T for B*T tokens, stored into slot `slot` of the
 // [B, Hkv, T, L, d] depth caches.
 struct KvWriteProblem {

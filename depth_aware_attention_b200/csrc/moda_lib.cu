@@ -7,3 +7,5 @@
 #include "moda_decode.cu"
 #include "moda_kvwrite.cu"
 #include "moda_tree.cu"
+#include "moda_score.cu"
+#include "moda_evict.cu"

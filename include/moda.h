@@ -225,6 +225,46 @@ moda_status_t moda_tree_decode(const void *q, const void *k, const void *v, cons
                                moda_stream_t stream);
 
 /*
+ * The attention weight that the newest N tokens of each sequence give to its cached keys,
+ * added to a running score per key and KV head (the pages describe no cache eviction; the
+ * weights are those of the joint softmax, whose normaliser lse includes the depth keys):
+ *   score_out[b][g][s] = score[b][g][s] + sum over heads h of group g and tokens i with
+ *                        s <= lengths[b] - N + i of exp(scale*<q[b,h,i], k[b,g,s]> - lse[b,h,i])
+ *   q: bf16 [B][Hq][N][d], the queries of the tokens at the cache's positions lengths[b]-N ..
+ *      lengths[b]-1     k: bf16 [B][Hkv][S][d]     lse: fp32 [B][Hq][N], as attention returned it
+ *   score, score_out: fp32 [B][Hkv][S]; score_out may be score itself, else no overlap
+ *   lengths: int32 [B], device, 0 <= lengths[b] <= S (rules and errors as moda_tree_decode)
+ * Tokens before the cache's start (N > lengths[b]) and rows whose lse is -inf carry no weight.
+ * Keys from lengths[b] on are not read into any result; their scores stay as they are
+ * (score_out != score: are copied).  Pointers of fp32 and int32 arrays need 4-byte alignment.
+ * N <= 128, Hq / Hkv <= 64, d in {64, 128} (MODA_ERR_UNSUPPORTED otherwise); scale > 0.  One
+ * launch per 3 * floor(128 / (Hq/Hkv)) tokens, no workspace; the same bits on every run.
+ */
+moda_status_t moda_cache_score(const void *q, const void *k, const float *lse,
+                               const int32_t *lengths, const float *score, float *score_out,
+                               int B, int Hq, int Hkv, int S, int N, int d, float scale,
+                               moda_stream_t stream);
+
+/*
+ * Eviction: every KV head's cache cut down to min(lengths[b], keep) entries, in their old
+ * order: the first `sinks`, the last `recent`, and of the others those with the highest score
+ * (ties to the lowest position; -0 counts as 0, a NaN as less than -inf).
+ *   k, v: bf16 [B][Hkv][S][d]   score: fp32 [B][Hkv][S]   lengths: int32 [B] (device; rules
+ *   and errors as moda_tree_decode)
+ *   k_out, v_out: bf16 [B][Hkv][keep][d], score_out: fp32 [B][Hkv][keep]: the kept entries
+ *   index: int32 [B][Hkv][keep], their old positions     lengths_out: int32 [B]
+ * Rows of the outputs from lengths_out[b] on are left as they are.  No output may overlap an
+ * input.  keep >= 1, sinks, recent >= 0, sinks + recent <= keep
+ * (MODA_ERR_INVALID_ARGUMENT otherwise); keep may exceed S.  K and V pointers 16-byte, the
+ * others 4-byte aligned.  Two launches, no workspace.
+ */
+moda_status_t moda_cache_evict(const void *k, const void *v, const float *score,
+                               const int32_t *lengths, void *k_out, void *v_out,
+                               float *score_out, int32_t *index, int32_t *lengths_out, int B,
+                               int Hkv, int S, int keep, int sinks, int recent, int d,
+                               moda_stream_t stream);
+
+/*
  * Fused depth-stream write: the projection that produces a sublayer's depth key/value
  * pair, with the depth cache as its output (hyper.ai summary of arXiv 2603.15619,
  * section "Hardware-efficient implementation": every layer appends its K/V to the
