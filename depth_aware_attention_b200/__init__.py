@@ -11,6 +11,7 @@ Low-level names mirror the C ABI (``moda_forward``, ``moda_backward``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -539,13 +540,14 @@ def _checked(device, specs, workspace=None):
 
 def _call(fn, name, device, *args):
     """Calls the C entry point `fn` with the current stream of `device`, which is made the
-    current device for the call when it is not."""
+    current device for the call when it is not.  (torch.cuda.current_stream() builds a Stream
+    object, 2 us of a small call's 15; the raw handle takes 0.1.)"""
     import torch
     if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if st != MODA_OK:
         raise ModaError(st, name, _msg(st))
 
@@ -630,6 +632,11 @@ def backward_packed(q, k, v, cu_seqlens, kd, vd, out, lse, dout, scale=None, cau
     return g
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace_size(*sizes):
+    return lib.moda_tree_decode_workspace_size(*sizes)
+
+
 def tree_decode(q, k, v, kt, vt, parents, lengths, kd=None, vd=None, scale=None, out=None,
                 lse=None, workspace=None):
     """Attention of N drafted tokens per sequence over a ragged cache, on the current CUDA
@@ -655,8 +662,8 @@ def tree_decode(q, k, v, kt, vt, parents, lengths, kd=None, vd=None, scale=None,
     if lse is None:
         lse = torch.empty((B, Hq, N), device=q.device, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(lib.moda_tree_decode_workspace_size(B, Hq, Hkv, S, N, L, d),
-                                device=q.device, dtype=torch.uint8)
+        workspace = torch.empty(_tree_workspace_size(B, Hq, Hkv, S, N, L, d), device=q.device,
+                                dtype=torch.uint8)
     bf, new = torch.bfloat16, (B, Hkv, N, d)
     spec = [("q", q, (B, Hq, N, d), bf), ("k", k, (B, Hkv, S, d), bf), ("v", v, (B, Hkv, S, d), bf),
             ("kt", kt, new, bf), ("vt", vt, new, bf), ("parents", parents, (B, N), torch.int32),

@@ -8,12 +8,13 @@
 // What bounds it: the copy of the kept rows (HBM), once the selection is quick.  Two launches:
 //   1. moda_evict_select_kernel: a radix selection.  A float's bits map to an integer of the
 //      same order; protected entries get the largest integer, so that one selection of the
-//      `keep` largest finds the whole set.  Three passes (11, 11 and 10 bits, from the top)
-//      each count the keys that still match the prefix into 2048 bins and step into the bin
-//      that holds the keep-th largest.  A row of scores is shared by a cluster of eight CTAs
-//      (one CTA for short rows), which add their counts over distributed shared memory.  Then
-//      each CTA writes its kept positions behind those of the CTAs before it: everything above
-//      the threshold, and of the entries equal to it the first that still fit.
+//      `keep` largest finds the whole set.  Four passes of 8 bits, from the top, each count the
+//      keys that still match the prefix into 256 bins and step into the bin that holds the
+//      keep-th largest.  A row of scores is shared by a cluster of eight CTAs (one CTA for short
+//      rows), which add their counts over distributed shared memory.  The keys are read from
+//      global memory once and stay in shared memory.  Then each warp, whose keys are a
+//      contiguous run, writes its kept positions behind those of the warps and CTAs before it:
+//      everything above the threshold, and of the entries equal to it the first that still fit.
 //   2. moda_evict_gather_kernel: the rows, 16 bytes a thread, every destination row its own
 //      work item, so that the copy runs at the whole GPU's rate however the kept entries lie.
 // Only counts go through atomics, so the result does not depend on their order.
@@ -30,10 +31,14 @@ namespace moda {
 
 namespace {
 
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictBins = 2048;
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
 // Rows of up to this many scores are one CTA's work; longer ones a cluster's.
-constexpr int kEvictOneCta = 4096;
+constexpr int kEvictOneCta = 8192;
+// Keys a CTA holds in shared memory (96 KB, so that two CTAs share an SM: with one CTA an SM
+// the clusters of 16 rows did not all fit the GPU at once).  Longer rows are read from global
+// memory in every pass.
+constexpr int kEvictHeld = 24576;
 
 struct EvictArgs {
   const uint4 *k, *v;
@@ -62,12 +67,17 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 
 // Cluster of kCl CTAs (1 or 8) per (sequence, KV head); CTA `rank` holds the positions
-// [rank * seg, (rank + 1) * seg).
-template <int kCl>
-__global__ void __launch_bounds__(kEvictThreads, 1) moda_evict_select_kernel(const EvictArgs a) {
+// [rank * seg, (rank + 1) * seg), its warp w a contiguous sixteenth of them.
+template <int kCl, bool kHeld>
+__global__ void __launch_bounds__(kEvictThreads, 2) moda_evict_select_kernel(const EvictArgs a) {
   namespace cg = cooperative_groups;
-  __shared__ __align__(16) int hist[3][kEvictBins];
-  __shared__ int wsum[32], wsum2[32];
+  extern __shared__ uint32_t held[];  // kHeld: this CTA's keys
+  // kCopies counters per bin, by lane, for the counting itself: scores crowd in a few bins (many
+  // are exactly zero), and the adds of one warp to one address come one after the other
+  constexpr int kCopies = 8;
+  __shared__ __align__(16) int tally[256 * kCopies];
+  __shared__ int hist[4][256];
+  __shared__ int wsum[kEvictWarps], wsum2[kEvictWarps];
   __shared__ int found_bin, found_above;
   __shared__ int counts[2];  // this CTA's keys above the threshold, and equal to it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -78,151 +88,146 @@ __global__ void __launch_bounds__(kEvictThreads, 1) moda_evict_select_kernel(con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int want = min(len, a.keep);
   if (rank == 0 && tid == 0 && bg % a.Hkv == 0) a.lengths_out[b] = want;
-  const int seg = ((len + kCl - 1) / kCl + 31) & ~31;
-  const int p0 = min(len, rank * seg), p1 = min(len, p0 + seg);
+  const int run = (((len + kCl - 1) / kCl + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  // this warp's positions [w0, w1)
+  const long long first = ((long long)rank * kEvictWarps + warp) * run;
+  const int w0 = int(min((long long)len, first)), w1 = int(min((long long)len, first + run));
   const float* const row = a.score + (long long)bg * a.S;
   int* const index = a.index + (long long)bg * a.keep;
   float* const score_out = a.score_out + (long long)bg * a.keep;
   if (len <= a.keep) {  // everything stays (the same decision in the whole cluster)
-    for (int p = p0 + tid; p < p1; p += kEvictThreads) {
+    for (int p = w0 + lane; p < w1; p += 32) {
       index[p] = p;
       score_out[p] = row[p];
     }
     return;
   }
   const int last = len - a.recent;
-  auto key_at = [&](int p) {
-    return p < a.sinks || p >= last ? 0xffffffffu : ordered(__ldg(row + p));
+  auto make_key = [&](int p) {
+    const uint32_t key = ordered(__ldg(row + p));
+    return p < a.sinks || p >= last ? 0xffffffffu : key;
   };
+  uint32_t* const mine = held + warp * run - w0;  // key of position p at mine[p]
+  auto key_at = [&](int p) { return kHeld ? mine[p] : make_key(p); };
   auto cluster_wait = [&]() {
     if constexpr (kCl > 1)
       cg::this_cluster().sync();
     else
       __syncthreads();
   };
-  for (int i = tid; i < 3 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < 256 * kCopies; i += kEvictThreads) tally[i] = 0;
+  if constexpr (kHeld) {
+    // (each warp reads and later uses only its own run)
+#pragma unroll 8
+    for (int p = w0 + lane; p < w1; p += 32) mine[p] = make_key(p);
+  }
   __syncthreads();
 
   uint32_t prefix = 0;  // the threshold's bits found so far, from the top
   int need = want;      // how many of the keys that match the prefix are to be kept
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    const uint32_t above = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
-    for (int p = p0 + tid; p < p1; p += kEvictThreads) {
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll 4
+    for (int p = w0 + lane; p < w1; p += 32) {
       const uint32_t key = key_at(p);
-      if ((key & above) == prefix) atomicAdd(&hist[pass][(key >> shift) & mask], 1);
+      if ((key & above) == prefix)
+        atomicAdd(&tally[((key >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int4* const t4 = reinterpret_cast<int4*>(tally + tid * kCopies);
+      const int4 x = t4[0], y = t4[1];
+      hist[pass][tid] = (x.x + x.y) + (x.z + x.w) + (y.x + y.y) + (y.z + y.w);
+      t4[0] = t4[1] = make_int4(0, 0, 0, 0);
     }
     cluster_wait();
-    // thread t: bins 2047 - 2t and 2046 - 2t, so that a prefix sum runs from the top bin down
-    const int hi_bin = kEvictBins - 1 - 2 * tid, lo_bin = hi_bin - 1;
-    int n_hi = 0, n_lo = 0;
-    if constexpr (kCl > 1) {
-      cg::cluster_group cluster = cg::this_cluster();
+    // thread t < 256: bin 255 - t, so that a prefix sum runs from the top bin down
+    int n = 0, incl = 0;
+    if (tid < 256) {
+      if constexpr (kCl > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
 #pragma unroll
-      for (int r = 0; r < kCl; ++r) {
-        const int2 x = *reinterpret_cast<const int2*>(
-            cluster.map_shared_rank(&hist[pass][0], r) + lo_bin);
-        n_lo += x.x;
-        n_hi += x.y;
+        for (int r = 0; r < kCl; ++r) n += cluster.map_shared_rank(&hist[pass][0], r)[255 - tid];
+      } else {
+        n = hist[pass][255 - tid];
       }
-    } else {
-      n_hi = hist[pass][hi_bin];
-      n_lo = hist[pass][lo_bin];
-    }
-    int incl = n_hi + n_lo;
+      incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) wsum[warp] = incl;
     }
-    if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    int base = wsum[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, base, o);
-      if (lane >= o) base += v;
-    }
-    const int before_warp = __shfl_sync(0xffffffffu, base, warp ? warp - 1 : 0);
-    const int before = (warp ? before_warp : 0) + incl - n_hi - n_lo;  // keys in higher bins
-    // exactly one bin holds the need-th largest of the matching keys
-    if (before < need && before + n_hi >= need) {
-      found_bin = hi_bin;
-      found_above = before;
-    } else if (before + n_hi < need && before + n_hi + n_lo >= need) {
-      found_bin = lo_bin;
-      found_above = before + n_hi;
+    if (tid < 256) {
+      const int before =
+          incl - n + __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane & 7] : 0);
+      // exactly one bin holds the need-th largest of the matching keys
+      if (before < need && before + n >= need) {
+        found_bin = 255 - tid;
+        found_above = before;
+      }
     }
     __syncthreads();
     prefix |= uint32_t(found_bin) << shift;
     need -= found_above;
-    __syncthreads();
   }
 
   // positions above the threshold all stay, and the first `need` of those equal to it
   int gt = 0, eq = 0;
-  for (int p = p0 + tid; p < p1; p += kEvictThreads) {
+#pragma unroll 4
+  for (int p = w0 + lane; p < w1; p += 32) {
     const uint32_t key = key_at(p);
     gt += key > prefix;
     eq += key == prefix;
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
+  __syncthreads();  // (wsum's last readers)
   if (lane == 0) {
     wsum[warp] = gt;
     wsum2[warp] = eq;
   }
   __syncthreads();
+  const int g = lane < kEvictWarps ? wsum[lane] : 0, e = lane < kEvictWarps ? wsum2[lane] : 0;
   if (warp == 0) {
-    const int g = __reduce_add_sync(0xffffffffu, wsum[lane]);
-    const int e = __reduce_add_sync(0xffffffffu, wsum2[lane]);
+    const int gs = __reduce_add_sync(0xffffffffu, g), es = __reduce_add_sync(0xffffffffu, e);
     if (lane == 0) {
-      counts[0] = g;
-      counts[1] = e;
+      counts[0] = gs;
+      counts[1] = es;
     }
   }
-  cluster_wait();
-  int at = 0, eq_before = 0;  // kept and equal keys of the CTAs before this one
+  // keys above and equal in the warps, then in the CTAs, before this one
+  int gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? g : 0);
+  int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
   if constexpr (kCl > 1) {
-    for (int r = 0; r < rank; ++r) {
-      const int* c = cg::this_cluster().map_shared_rank(&counts[0], r);
-      const int g = c[0], e = c[1];
-      at += g + min(max(need - eq_before, 0), e);
-      eq_before += e;
-    }
+    cg::this_cluster().sync();
+    const int* c = cg::this_cluster().map_shared_rank(&counts[0], lane < rank ? lane : rank);
+    gt_before += __reduce_add_sync(0xffffffffu, lane < rank ? c[0] : 0);
+    eq_before += __reduce_add_sync(0xffffffffu, lane < rank ? c[1] : 0);
     // (a CTA must not leave while another still reads its counts)
     cg::this_cluster().barrier_arrive();
   }
-  for (int q0 = p0; q0 < p1; q0 += kEvictThreads) {
-    const int p = q0 + tid;
-    const uint32_t key = p < p1 ? key_at(p) : 0u;
-    const bool is_gt = p < p1 && key > prefix, is_eq = p < p1 && key == prefix;
-    const uint32_t bg_gt = __ballot_sync(0xffffffffu, is_gt);
-    const uint32_t bg_eq = __ballot_sync(0xffffffffu, is_eq);
-    if (lane == 0) {
-      wsum[warp] = __popc(bg_gt);
-      wsum2[warp] = __popc(bg_eq);
-    }
-    __syncthreads();
-    // sums over the warps before this one, and over all of them
-    const int g = wsum[lane], e = wsum2[lane];
-    const int eq_w = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
-    const int gt_w = __reduce_add_sync(0xffffffffu, lane < warp ? g : 0);
-    const int eq_all = __reduce_add_sync(0xffffffffu, e);
-    const int gt_all = __reduce_add_sync(0xffffffffu, g);
-    const uint32_t below = (1u << lane) - 1u;
-    const int eq_mine = eq_before + eq_w + __popc(bg_eq & below);  // equal keys before p
-    if (is_gt || (is_eq && eq_mine < need)) {
-      const int kept_eq = min(eq_mine, need) - min(eq_before, need);
-      const int dst = at + gt_w + __popc(bg_gt & below) + kept_eq;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int q = w0; q < w1; q += 32) {
+    const int p = q + lane;
+    const uint32_t key = p < w1 ? key_at(p) : 0u;
+    const float score = p < w1 ? __ldg(row + p) : 0.f;
+    const uint32_t m_gt = __ballot_sync(0xffffffffu, p < w1 && key > prefix);
+    const uint32_t m_eq = __ballot_sync(0xffffffffu, p < w1 && key == prefix);
+    const int eq_mine = eq_before + __popc(m_eq & below);  // equal keys before p
+    const bool is_eq = (m_eq >> lane) & 1u;
+    if (((m_gt >> lane) & 1u) || (is_eq && eq_mine < need)) {
+      const int dst = gt_before + __popc(m_gt & below) + min(eq_mine, need);
       index[dst] = p;
-      score_out[dst] = row[p];
+      score_out[dst] = score;
     }
-    at += gt_all + min(eq_before + eq_all, need) - min(eq_before, need);
-    eq_before += eq_all;
-    __syncthreads();
+    gt_before += __popc(m_gt);
+    eq_before += __popc(m_eq);
   }
   if constexpr (kCl > 1) cg::this_cluster().barrier_wait();
 }
@@ -257,11 +262,13 @@ __global__ void __launch_bounds__(256) moda_evict_gather_kernel(const EvictArgs 
     }
 }
 
-template <int kCl>
+template <int kCl, bool kHeld>
 cudaError_t launch_select(const EvictArgs& a, cudaStream_t stream) {
+  const int run = (((a.S + kCl - 1) / kCl + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.B) * a.Hkv * kCl);
   cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = kHeld ? size_t(run) * kEvictWarps * 4 : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -270,7 +277,11 @@ cudaError_t launch_select(const EvictArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moda_evict_select_kernel<kCl>, a);
+  cudaError_t e = cudaFuncSetAttribute(moda_evict_select_kernel<kCl, kHeld>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(cfg.dynamicSmemBytes));
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, moda_evict_select_kernel<kCl, kHeld>, a);
 }
 
 }  // namespace
@@ -295,7 +306,9 @@ cudaError_t launch_evict(const EvictProblem& p, const void* k, const void* v, co
   a.sinks = p.sinks;
   a.recent = p.recent;
   a.chunks = p.d / 8;
-  cudaError_t e = p.S <= kEvictOneCta ? launch_select<1>(a, stream) : launch_select<8>(a, stream);
+  cudaError_t e = p.S <= kEvictOneCta       ? launch_select<1, true>(a, stream)
+                  : (p.S + 7) / 8 <= kEvictHeld - 512 ? launch_select<8, true>(a, stream)
+                                                      : launch_select<8, false>(a, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     *why = "eviction's selection launch failed";

@@ -137,6 +137,44 @@ __device__ __forceinline__ ScoreWalk score_first(const ScoreArgs& a, long long s
   return w;
 }
 
+// This warpgroup's part of the scores behind each length, copied when score_out is not score:
+// units of 1024 scores, one beside each key block (loaded before the block's weights are
+// waited for and stored after them, so that it costs no time of its own), the rest at the end.
+struct TailCopy {
+  static constexpr int kEach = 8;  // scores per thread of a unit
+  int u, units, per, at;
+  __device__ __forceinline__ TailCopy(const ScoreArgs& a, int wg, int thread) {
+    per = (a.S + 1023) / 1024;
+    units = a.copy_tail ? a.B * a.Hkv * per : 0;
+    u = 2 * blockIdx.x + wg;
+    at = thread;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(const ScoreArgs& a, F f) const {
+    const int bg = u / per, c = u - bg * per;
+    const int lo = score_length(a, bg / a.Hkv);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int p = c * 1024 + i * 128 + at;
+      if (p >= lo && p < a.S) f(i, (long long)bg * a.S + p);
+    }
+  }
+  __device__ __forceinline__ void load(const ScoreArgs& a, float (&x)[kEach]) const {
+    if (u < units) each(a, [&](int i, long long p) { x[i] = a.score[p]; });
+  }
+  __device__ __forceinline__ void store(const ScoreArgs& a, const float (&x)[kEach]) {
+    if (u < units) each(a, [&](int i, long long p) { a.score_out[p] = x[i]; });
+    u += 2 * gridDim.x;
+  }
+  __device__ __forceinline__ void rest(const ScoreArgs& a) {
+    while (u < units) {
+      float x[kEach];
+      load(a, x);
+      store(a, x);
+    }
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     moda_score_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -158,20 +196,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (a.copy_tail) {
-    // scores behind each length, in units of 4096
-    const int per = (a.S + 4095) / 4096;
-    const long long units = (long long)a.B * a.Hkv * per;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-      const int bg = int(u / per), c = int(u - (long long)bg * per);
-      const long long row = (long long)bg * a.S;
-      const int e = min(a.S, (c + 1) * 4096);
-      for (int i = max(score_length(a, bg / a.Hkv), c * 4096) + int(threadIdx.x); i < e;
-           i += kScoreThreads)
-        a.score_out[row + i] = a.score[row + i];
-    }
-  }
-
+  if (warp == 8 && lane < 2) tma_prefetch_desc(lane ? &tmQ : &tmK);
   long long n = 0;
   for (int b = lane; b < a.B; b += 32) n += score_blocks(a, b);
 #pragma unroll
@@ -181,7 +206,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const long long first = share * blockIdx.x;
   if (blockIdx.x == 0 && warp == 0)
     for (int b = lane; b < a.B; b += 32) score_length(a, b, true);
-  if (first >= total) return;
+  if (first >= total) {  // no block for this CTA; its part of the tails is left
+    TailCopy tail(a, threadIdx.x >> 7, threadIdx.x & 127);
+    if (threadIdx.x < 256) tail.rest(a);
+    return;
+  }
   const ScoreWalk walk0 = score_first(a, first, min(share, total - first));
 
   if (threadIdx.x == 0) {
@@ -306,12 +335,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             const float x = __ldg(a.lse + ((long long)w.b * a.Hq + w.g * a.G + r - tok * a.G) * a.N + i);
             if (x != -INFINITY) v = x * kLog2eScore;  // -inf: a row that saw nothing
           }
-          if (r < a.TQ * a.G) lse2[t * 128 + r] = v;
-          uint32_t none = __ballot_sync(0xffffffffu, r < a.TQ * a.G && v == INFINITY);
-          for (; none; none &= none - 1) {
-            const int z = r0 + __ffs(none) - 1;
-            zero_tile_rows(sQ(t), Cfg::kRegions, z, z + 1);
-          }
+          if (in) lse2[t * 128 + r] = v;
+          // rows [.., ntok) without a weight, zeroed; the rows behind them are never summed
+          const bool none = in && v == INFINITY;
+          if (__any_sync(0xffffffffu, none))
+            for (int z = 0; z < 32; ++z)
+              if (__shfl_sync(0xffffffffu, none, z))
+                zero_tile_rows(sQ(t), Cfg::kRegions, r0 + z, r0 + z + 1);
         }
       publish_rows(bar(bars->q_ready));
     }
@@ -322,6 +352,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int key = threadIdx.x & 127;  // TMEM lane = key of the block
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + wg * 256;
     ScoreWalk w = walk0;
+    TailCopy tail(a, wg, key);
     uint32_t uo = 0;
     int pc = 0;
     bool more = true;
@@ -329,6 +360,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       mbar_wait(bar(bars->q_ready), pc & 1, abort_flag);  // lse2
       const long long row = ((long long)w.b * a.Hkv + w.g) * a.S;
       for (int j = w.j0 + wg; j < w.j1; j += 2) {
+        float moved[TailCopy::kEach];
+        tail.load(a, moved);
         const int s = j * 128 + key;  // position of this thread's key
         const bool inside = s < w.len;
         const float old = inside ? a.score[row + s] : 0.f;  // (may be score_out)
@@ -381,11 +414,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           if (lane == 0) mbar_arrive(bar(bars->s_free[wg][uo & 1]));
         }
         if (inside) a.score_out[row + s] = old + (sum.x + sum.y);
+        tail.store(a, moved);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->q_empty));
       more = w.next(a);
     }
+    tail.rest(a);
   }
 
   tc_fence_before();

@@ -232,6 +232,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile int* abort_flag = &bars->abort;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8 && lane < 7) {
+    const CUtensorMap* maps[7] = {&tmQ, &tmK, &tmV, &tmKT, &tmVT, &tmKD, &tmVD};
+    tma_prefetch_desc(maps[lane]);
+  }
 
   long long total;
   const long long share = tree_share(a, total);
@@ -259,14 +263,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     bars->abort = 0;
     fence_barrier_init();
   }
-  // Q rows past TQ*G never receive TMA data: zero them once
-  if (threadIdx.x < 128 && threadIdx.x >= a.TQ * a.G) {
-    for (int t = 0; t < Cfg::kQTiles * Cfg::kRegions; ++t)
-      for (int c = 0; c < 8; ++c)
-        sts128(s0 + uint32_t(t) * kTreeRegion + threadIdx.x * 128u + c * 16u,
-               make_uint4(0u, 0u, 0u, 0u));
-    fence_proxy_async_smem();
-  }
+  // (Q rows past TQ*G never receive data: whatever lies there only makes rows of S, P and O
+  // that nothing reads)
   if (warp == 9) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();

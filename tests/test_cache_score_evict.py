@@ -145,7 +145,10 @@ EVICTS = [
     ("cluster-special", [33333, 33332], 33333, 12345, 1, 1, 1, 64, "special"),
     ("cluster-all-protected", [10000], 10000, 600, 100, 500, 2, 64, "weights"),
     ("cluster-one-left", [8193], 8193, 8192, 0, 8191, 1, 64, "weights"),
+    ("one-cta-odd", [8191, 8192], 8192, 4095, 5, 77, 1, 64, "special"),
+    ("cluster-8193", [8193, 8000], 8193, 100, 5, 77, 1, 64, "ties"),
     ("long", [131072, 100], 131072, 30000, 4, 1000, 1, 64, "ties"),
+    ("not-held", [200001, 150, 60000], 200001, 30000, 4, 1000, 1, 64, "special"),
 ]
 
 
