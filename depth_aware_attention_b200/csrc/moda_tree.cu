@@ -81,7 +81,7 @@ struct TreeArgs {
 struct TreeBars {
   uint64_t full[10], empty[10], ready[10];  // ring: landed; released; zeroed where needed
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2];
   uint64_t o_final, o_free;
   uint64_t drain;
   uint32_t tmem_base;
@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     mbar_init(bar(bars->q_empty), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(bars->s_full[t]), 1);
-      mbar_init(bar(bars->p_full[t]), 4);  // one arrival a warp
+      mbar_init(bar(bars->p_half[t]), 4);  // one arrival a warp
+      mbar_init(bar(bars->p_full[t]), 4);
     }
     mbar_init(bar(bars->o_final), 1);
     mbar_init(bar(bars->o_free), 8);
@@ -389,18 +390,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool two = wide(c.j);
         const int e = c.e + (two ? 2 + c.half : 1);
         mbar_wait(bar(bars->ready[e % NS]), (e / NS) & 1, abort_flag);
-        mbar_wait(bar(bars->p_full[wg]), (c.u >> 1) & 1, abort_flag);
         // the accumulators of the piece before have been read
         if (c.pc > 0 && c.j == c.w.j0 && c.half == 0)
           mbar_wait(bar(bars->o_free), (c.pc - 1) & 1, abort_flag);
-        tc_fence_after();
         // this warpgroup's first product of the piece overwrites its accumulator
         const bool fresh = kPair ? c.j == c.w.j0 : c.j - c.w.j0 < 2;
+        // keys [0, 64) as soon as their P is in, then the rest
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + ks * 8,
-                 make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
-                 (ks > 0 || !fresh) ? 1u : 0u);
+        for (int half = 0; half < 2; ++half) {
+          mbar_wait(bar(half ? bars->p_full[wg] : bars->p_half[wg]), (c.u >> 1) & 1, abort_flag);
+          tc_fence_after();
+#pragma unroll
+          for (int kq = 0; kq < 4; ++kq) {
+            const int ks = half * 4 + kq;
+            mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + ks * 8,
+                   make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
+                   (ks > 0 || !fresh) ? 1u : 0u);
+          }
+        }
         if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
         if (c.j == c.w.j1 - 1 && (!kPair || c.half == 1)) tc_commit(bar(bars->o_final));
         advance(c);
@@ -471,6 +478,137 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + wg * 128;
     const uint32_t tO = tmem + lane_base + 256 + wg * D;
+    float m = -INFINITY, l = 0.f;  // this row's running maximum (log2 units) and sum
+    bool has_o = false;
+    // O is rescaled before the first half of P is published, since that half's product may
+    // start at once.  (Every product of this warpgroup so far was issued before its S and has
+    // finished.)
+    auto rescale_o = [&](bool grow, float alpha) {
+      if (__any_sync(0xffffffffu, grow && has_o)) {
+        const float f = grow ? alpha : 1.f;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t o[16];
+          tmem_ld16(tO + cc * 16, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st16(tO + cc * 16, o);
+        }
+      }
+      has_o = true;
+    };
+    auto publish = [&](uint64_t& b) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    // P enters its product as bf16 (the products' operand type); l sums it unrounded.
+    // A cache block that lies inside the cache: no mask, every fourth pair of exponentials on
+    // the FMA pipe, as in the forward.
+    auto full_step = [&]() {
+      uint32_t s[128];
+      tmem_ld32(tS + 0, &s[0]);
+      tmem_ld32(tS + 32, &s[32]);
+      tmem_ld32(tS + 64, &s[64]);
+      tmem_ld32(tS + 96, &s[96]);
+      tmem_wait_ld();
+      float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 128; c += 4) {
+        mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+      }
+      const float m_cand = fmaxf(m, fmaxf(mx, mx1) * a.scale_log2);
+      const bool grow = m_cand > m + kTreeRescale;
+      const float m_new = grow ? m_cand : m;
+      const float alpha = ex2(m - m_new);
+      const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+      const float2 nm2 = make_float2(-m_new, -m_new);
+      float2 ps = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 x = ffma2(make_float2(__uint_as_float(s[half * 64 + c]),
+                                             __uint_as_float(s[half * 64 + c + 1])),
+                                 sl2, nm2);
+          const float2 p = (c / 2) % kExpFmaPeriod == kExpFmaPeriod - 1
+                               ? exp2_fma2(x)
+                               : make_float2(ex2(x.x), ex2(x.y));
+          ps = fadd2(ps, p);
+          pk[c / 2] = pack_bf16x2(p.x, p.y);
+        }
+        if (half == 0) rescale_o(grow, alpha);
+        tmem_st32(tS + half * 32, pk);
+        publish(half ? bars->p_full[wg] : bars->p_half[wg]);
+      }
+      l = l * alpha + (ps.x + ps.y);
+      m = m_new;
+    };
+    // Any other step: 32 keys at a time, those no row of the warp sees skipped.  P's columns of
+    // a chunk overwrite S columns that were read before.
+    auto masked_step = [&](const TreeWalk& w, int j, int ti, const int* par) {
+      uint32_t vis[4];
+      if (j < a.ND) {
+        const int lo = tok * a.JC, nv = min(a.JC, a.L - j * a.JC);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) vis[q] = range_bits(lo, lo + nv, q);
+      } else if (j == a.ND) {
+        vis[0] = vis[1] = vis[2] = vis[3] = 0u;
+        if (tok < a.TQ && ti < a.N) ancestor_bits(par, ti, vis);
+      } else {
+        const int inside = w.len - (j - a.ND - 1) * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) vis[q] = range_bits(0, inside, q);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (!__any_sync(0xffffffffu, vis[q] != 0u)) continue;
+        uint32_t s[32];
+        tmem_ld32(tS + 32 * q, s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if ((vis[q] >> c) & 1u) mx = fmaxf(mx, __uint_as_float(s[c]));
+      }
+      const float m_cand = fmaxf(m, mx * a.scale_log2);
+      const bool grow = m_cand > m + kTreeRescale;
+      const float m_new = grow ? m_cand : m;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = ex2(m - m_use);
+      float ps = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+        if (__any_sync(0xffffffffu, vis[q] != 0u)) {
+          uint32_t s[32];
+          tmem_ld32(tS + 32 * q, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float x0 = fmaf(__uint_as_float(s[c]), a.scale_log2, -m_use);
+            const float x1 = fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -m_use);
+            const float p0 = ex2((vis[q] >> c) & 1u ? x0 : -INFINITY);
+            const float p1 = ex2((vis[q] >> c) & 2u ? x1 : -INFINITY);
+            ps += p0 + p1;
+            pk[c / 2] = pack_bf16x2(p0, p1);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = 0u;
+        }
+        if (q == 0) rescale_o(grow, alpha);
+        tmem_st16(tS + 16 * q, pk);
+        if (q == 1) publish(bars->p_half[wg]);
+        if (q == 3) publish(bars->p_full[wg]);
+      }
+      l = l * alpha + ps;
+      m = m_new;
+    };
     TreeWalk w = walk0;
     int u = 0;  // unit
     int pc = 0;
@@ -485,92 +623,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool valid = tok < a.TQ && ti < a.N;
       // warps without a row in the tile only keep the barriers in step
       const bool active = (warp & 3) * 32 < min(a.TQ, a.N - t0) * a.G;
-      float m = -INFINITY, l = 0.f;
-      bool has_o = false;
+      m = -INFINITY;
+      l = 0.f;
+      has_o = false;
       for (int j = w.j0; j < w.j1; ++j) {
         if (!kPair && ((u + j - w.j0) & 1) != wg) continue;
         const int unit = kPair ? u + 2 * (j - w.j0) + wg : u + j - w.j0;
         mbar_wait(bar(bars->s_full[wg]), (unit >> 1) & 1, abort_flag);
         tc_fence_after();
         if (active) {
-          uint32_t s[128];
-          tmem_ld32(tS + 0, &s[0]);
-          tmem_ld32(tS + 32, &s[32]);
-          tmem_ld32(tS + 64, &s[64]);
-          tmem_ld32(tS + 96, &s[96]);
-          uint32_t vis[4];
-          bool masked = true;
-          if (j < a.ND) {
-            const int lo = tok * a.JC, nv = min(a.JC, a.L - j * a.JC);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) vis[q] = valid ? range_bits(lo, lo + nv, q) : 0u;
-          } else if (j == a.ND) {
-            if (valid)
-              ancestor_bits(par, ti, vis);
-            else
-              vis[0] = vis[1] = vis[2] = vis[3] = 0u;
-          } else {
-            const int inside = w.len - (j - a.ND - 1) * 128;
-            masked = inside < 128;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) vis[q] = range_bits(0, inside, q);
+          const int kbase = (j - a.ND - 1) * 128;
+          if (j > a.ND && kbase + 128 <= w.len)
+            full_step();
+          else
+            masked_step(w, j, ti, par);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(bars->p_half[wg]));
+            mbar_arrive(bar(bars->p_full[wg]));
           }
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
-          }
-          float mx = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          }
-          const float m_cand = fmaxf(m, fmaxf(mx, mx1) * a.scale_log2);
-          const bool grow = m_cand > m + kTreeRescale;
-          const float m_new = grow ? m_cand : m;
-          const float m_use = m_new == -INFINITY ? 0.f : m_new;
-          const float alpha = ex2(m - m_use);
-          // every product of this warpgroup so far was issued before its S and has finished
-          if (__any_sync(0xffffffffu, grow && has_o)) {
-            const float f = grow ? alpha : 1.f;
-#pragma unroll 1
-            for (int cc = 0; cc < D / 16; ++cc) {
-              uint32_t o[16];
-              tmem_ld16(tO + cc * 16, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(tO + cc * 16, o);
-            }
-          }
-          const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-          const float2 nm2 = make_float2(-m_use, -m_use);
-          float2 ps = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // P enters its product as bf16 (the products' operand type); l sums it unrounded
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const float2 x = ffma2(make_float2(__uint_as_float(s[half * 64 + c]),
-                                                 __uint_as_float(s[half * 64 + c + 1])),
-                                     sl2, nm2);
-              const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              ps = fadd2(ps, p);
-              pk[c / 2] = pack_bf16x2(p.x, p.y);
-            }
-            tmem_st32(tS + half * 32, pk);
-          }
-          l = l * alpha + (ps.x + ps.y);
-          m = m_new;
-          has_o = true;
-          tmem_wait_st();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars->p_full[wg]));
       }
       // ---- the piece's end
       const int units = (w.j1 - w.j0) * Cfg::kQTiles;
@@ -634,10 +708,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 dst[q] = pack8(x, inv);
               }
             } else {
-              float4* dst = reinterpret_cast<float4*>(a.ws_acc + wrow * D + col0 + cc * 32);
+              // 32 bytes a store: a row's columns come from one thread, so that a narrower
+              // store would fill its sectors in two goes
+              float* const dst = a.ws_acc + wrow * D + col0 + cc * 32;
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              for (int q = 0; q < 4; ++q) stg256(dst + 8 * q, &v[8 * q]);
             }
           }
         }
