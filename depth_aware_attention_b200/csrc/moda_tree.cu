@@ -19,7 +19,9 @@
 //   entries of its tokens (each row sees its own token's), the new tokens (each row sees its
 //   ancestors), the cache blocks.  All run through one TMA ring into the tensor cores.
 //   Split.  The steps of all items are laid in one line and cut into equal shares, one per
-//   CTA, whatever the lengths are: a CTA may end one item and begin the next.  The lengths
+//   CTA, whatever the lengths are: a CTA may end one item and begin the next.  Where whole
+//   CTAs per item leave shares hardly longer, each CTA has a part of one item instead
+//   (TreePlan).  The lengths
 //   are read on the device, so a captured graph follows them.  An item inside one CTA is
 //   written directly; the pieces of a cut item go to the workspace as (maximum, sum, fp32
 //   accumulator) and a second launch joins them, in the order of the steps.
@@ -104,14 +106,56 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// Steps of all sequences' items together, and the share of one CTA (all lanes of a warp).
-__device__ __forceinline__ long long tree_share(const TreeArgs& a, long long& total) {
+// How the steps are cut, the same in every CTA and in the joining kernel.
+//   parts == 0: all items' steps in one line, `share` of them per CTA;
+//   parts != 0: each item by itself into ceil(steps / share) equal parts, one per CTA, with the
+//               smallest share for which the parts do not outnumber the CTAs.
+// A CTA with two pieces drains the tensor cores, reads out and writes its accumulators twice,
+// which costs about as much as kTreeSwitch steps: the second way is taken when its shares are
+// at most that much longer.  (16 items of 10 steps: 80 CTAs of 2 steps; 16 of about 420 steps
+// each: shares of 49 instead of 46.)
+constexpr int kTreeSwitch = 3;
+struct TreePlan {
+  long long total, share;
+  int parts;
+  // CTAs of each item of a sequence with n steps per item, and the steps of each of them
+  __device__ __forceinline__ int ctas(int n) const { return int((n + share - 1) / share); }
+  __device__ __forceinline__ int each(int n) const {
+    const int c = ctas(n);
+    return (n + c - 1) / c;
+  }
+};
+
+// (all lanes of a warp)
+__device__ __forceinline__ TreePlan tree_plan(const TreeArgs& a) {
   const int lane = threadIdx.x & 31;
-  long long n = 0;
-  for (int b = lane; b < a.B; b += 32) n += tree_steps(a, b);
-  total = warp_sum(n) * a.nit;
-  const long long share = (total + kTreeCtas - 1) / kTreeCtas;
-  return share < kTreeMinShare ? kTreeMinShare : share;
+  TreePlan p;
+  long long sum = 0;
+  int most = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const int n = tree_steps(a, b);
+    sum += n;
+    most = max(most, n);
+  }
+  p.total = warp_sum(sum) * a.nit;
+  p.share = (p.total + kTreeCtas - 1) / kTreeCtas;
+  if (p.share < kTreeMinShare) p.share = kTreeMinShare;
+  p.parts = 0;
+  if ((long long)a.B * a.nit <= kTreeCtas) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    // (a share of p.share + kTreeSwitch or more is not taken, so the search may end there)
+    const int limit = min(int(p.share) + kTreeSwitch, most);
+    for (int share = int(p.share); share <= limit; ++share) {
+      int c = 0;
+      for (int b = lane; b < a.B; b += 32) c += (tree_steps(a, b) + share - 1) / share;
+      if (__reduce_add_sync(0xffffffffu, c) * a.nit <= kTreeCtas) {
+        p.share = share;
+        p.parts = 1;
+        break;
+      }
+    }
+  }
+  return p;
 }
 
 // A CTA's walk over its share: piece by piece, each a run of steps of one item.
@@ -138,17 +182,20 @@ struct TreeWalk {
   }
 };
 
-// The first piece of the share [s, s + left) (all lanes of a warp; left > 0).
-__device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, long long s, long long left) {
+// This CTA's first piece (all lanes of a warp); left < 0: there is none.
+__device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, const TreePlan& p) {
   const int lane = threadIdx.x & 31;
+  // steps, or with parts CTAs, before this CTA's; counted per item of each sequence
+  const long long s = p.parts ? blockIdx.x : p.share * blockIdx.x;
   TreeWalk w;
-  w.left = left;
-  long long before = 0;  // steps of one item of each earlier sequence
-  w.b = 0;
+  w.left = p.parts ? 0 : min(p.share, p.total - s);
+  long long before = 0;
+  w.b = a.B;
   w.it = 0;
   w.j0 = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0;
+    const int steps = b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0;
+    const int mine = p.parts ? p.ctas(steps) : steps;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,11 +212,19 @@ __device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, long long s, l
       w.b = b0 + src;
       w.it = int(off / n);
       w.j0 = int(off - (long long)w.it * n);
+      if (p.parts) {
+        const int all = __shfl_sync(0xffffffffu, steps, src), each = p.each(all);
+        w.left = min(each, all - w.j0 * each);
+        w.j0 *= each;
+      }
       break;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  w.clip(a);
+  if (w.b == a.B || w.left <= 0)
+    w.left = -1;
+  else
+    w.clip(a);
   return w;
 }
 
@@ -237,13 +292,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tma_prefetch_desc(maps[lane]);
   }
 
-  long long total;
-  const long long share = tree_share(a, total);
-  const long long first = share * blockIdx.x;
-  if (first >= total) return;
-  const TreeWalk walk0 = tree_first(a, first, min(share, total - first));
+  const TreeWalk walk0 = tree_first(a, tree_plan(a));
   if (blockIdx.x == 0 && warp == 0)
     for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
+  if (walk0.left < 0) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -747,24 +799,35 @@ __global__ void __launch_bounds__(256) moda_tree_join_kernel(const TreeArgs a, i
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= (long long)a.B * a.Hq * a.N) return;
-  long long total;
-  const long long share = tree_share(a, total);
+  const TreePlan plan = tree_plan(a);
   const int i = int(row % a.N);
   const int h = int(row / a.N % a.Hq), b = int(row / a.N / a.Hq);
   const int g = h / a.G, hl = h - g * a.G;
-  long long before = 0;
-  for (int x = lane; x < b; x += 32) before += tree_steps(a, x);
-  before = warp_sum(before) * a.nit;
   const int n = tree_steps(a, b);
   const int tile = i / a.TQ, item = g * a.nt + tile / qtiles;
-  const long long s = before + (long long)item * n;
-  const int c0 = int(s / share), c1 = int((s + n - 1) / share);
+  long long before = 0;
+  for (int x = lane; x < b; x += 32) {
+    const int m = tree_steps(a, x);
+    before += plan.parts ? plan.ctas(m) : m;
+  }
+  before = warp_sum(before) * a.nit;
+  const int each = plan.parts ? plan.ctas(n) : n;
+  const long long s = before + (long long)item * each;
+  int c0, c1;  // the CTAs that hold this item
+  if (plan.parts) {
+    c0 = int(s);
+    // (its parts that are not empty)
+    c1 = c0 + (n + plan.each(n) - 1) / plan.each(n) - 1;
+  } else {
+    c0 = int(s / plan.share);
+    c1 = int((s + n - 1) / plan.share);
+  }
   // the pieces' grid: wait for its completion
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;
   const int r = (tile % qtiles) * a.TQ * a.G + (i - tile * a.TQ) * a.G + hl;
   auto slot_row = [&](int c) {
-    return (long long)(2 * c + (s > c * share ? 1 : 0)) * a.rows + r;
+    return (long long)(2 * c + (!plan.parts && s > c * plan.share ? 1 : 0)) * a.rows + r;
   };
   float M = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ws_ml[slot_row(c) * 2]);
