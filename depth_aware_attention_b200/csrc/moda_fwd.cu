@@ -41,7 +41,8 @@
 //            seen S_t(j+1) know PV_t(j) has finished, so rescaling O_t needs no extra wait.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
 //
-// Packed batches (template flag kPacked): sequences of different lengths lie one behind the
+// Packed batches (template flag kPacked, dense path only; small batches and groups without a
+// dense path run on the tree attention's kernel): sequences of different lengths lie one behind the
 // other in one token axis of N rows.  A CTA's pair of tiles belongs to one sequence (found by
 // packed_find), whose first row is added to every coordinate; the rest of the kernel sees a
 // problem of that sequence's length.  A sequence's last V block and last depth blocks reach
@@ -378,14 +379,14 @@ __global__ void __launch_bounds__(kPacked ? kFwdPackedThreads : kFwdThreads, 1)
       for (int idx = 0; idx < kDPrefetch && idx < nuse; ++idx) {
         const CUtensorMap* map; int x, y;
         box(idx, map, x, y);
-        tma_prefetch_l2_4d(map, x, y, row0 + (t ? tq1 : tq0), bg);
+        tma_prefetch_l2_4d(map, x, y, t ? tq1 : tq0, bg);
       }
       int issued = 0;
       for (int idx = 0; idx < nuse; ++idx) {
         if (idx + kDPrefetch < nuse) {
           const CUtensorMap* pmap; int px, py;
           box(idx + kDPrefetch, pmap, px, py);
-          tma_prefetch_l2_4d(pmap, px, py, row0 + (t ? tq1 : tq0), bg);
+          tma_prefetch_l2_4d(pmap, px, py, t ? tq1 : tq0, bg);
         }
         const int s = idx % NDS;
         if (idx >= NDS &&
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kPacked ? kFwdPackedThreads : kFwdThreads, 1)
         const int rg = u % Cfg::kRegions;
         mbar_expect_tx(bar(bars->dfull[t][s]), dbytes);
         tma_load_4d(sDS(t, s), map, bar(bars->dfull[t][s]), rg * 64, (idx / kDUses) * a.JC,
-                    row0 + (t ? tq1 : tq0), bg);
+                    t ? tq1 : tq0, bg);
         issued = idx + 1;
       }
       if (*abort_flag) {
@@ -951,19 +952,25 @@ cudaError_t launch_forward(const Problem& p, const void* q, const void* k, const
                            const char** why) {
   const bool dense = depth_path == kDepthPathDense ||
                      (depth_path == kDepthPathAuto && dense_depth_default(p));
-  auto launch = [&](auto packed_c) {
-    constexpr bool kP = decltype(packed_c)::value;
-    if (p.d == 128)
-      return dense ? launch_forward_d<128, true, kP>(p, q, k, v, kd, vd, out, lse, encode,
-                                                     stream, why)
-                   : launch_forward_d<128, false, kP>(p, q, k, v, kd, vd, out, lse, encode,
-                                                      stream, why);
-    return dense
-               ? launch_forward_d<64, true, kP>(p, q, k, v, kd, vd, out, lse, encode, stream, why)
-               : launch_forward_d<64, false, kP>(p, q, k, v, kd, vd, out, lse, encode, stream,
-                                                 why);
-  };
-  return p.cu ? launch(std::true_type{}) : launch(std::false_type{});
+  if (p.cu) {
+    const PromptTile tile = prompt_tile(p);
+    if (tile.tokens > 0)
+      return launch_prompt(p, tile, q, k, v, kd, vd, out, lse, encode, stream, why);
+    // (with L = 0 the dense path is the same kernel without depth rings: more K/V stages)
+    return p.d == 128 ? launch_forward_d<128, true, true>(p, q, k, v, kd, vd, out, lse, encode,
+                                                          stream, why)
+                      : launch_forward_d<64, true, true>(p, q, k, v, kd, vd, out, lse, encode,
+                                                         stream, why);
+  }
+  if (p.d == 128)
+    return dense ? launch_forward_d<128, true, false>(p, q, k, v, kd, vd, out, lse, encode,
+                                                      stream, why)
+                 : launch_forward_d<128, false, false>(p, q, k, v, kd, vd, out, lse, encode,
+                                                       stream, why);
+  return dense ? launch_forward_d<64, true, false>(p, q, k, v, kd, vd, out, lse, encode, stream,
+                                                   why)
+               : launch_forward_d<64, false, false>(p, q, k, v, kd, vd, out, lse, encode, stream,
+                                                    why);
 }
 
 }  // namespace moda

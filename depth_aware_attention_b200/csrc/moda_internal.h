@@ -95,6 +95,17 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
                         void* workspace, EncodeTiledFn encode, cudaStream_t stream,
                         const char** why);
 
+// Packed forwards that the tree attention's kernel serves better than the forward's: the tokens
+// of a tile (0: the forward kernel's case) and whether a CTA takes a pair of tiles.
+struct PromptTile {
+  int tokens;
+  bool pair;
+};
+PromptTile prompt_tile(const Problem& p);
+cudaError_t launch_prompt(const Problem& p, const PromptTile& tile, const void* q, const void* k,
+                          const void* v, const void* kd, const void* vd, void* out, float* lse,
+                          EncodeTiledFn encode, cudaStream_t stream, const char** why);
+
 // The weight that the newest N queries of each sequence give to its cached keys.
 struct ScoreProblem {
   int B, Hq, Hkv, S, N, d;

@@ -37,6 +37,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "moda_internal.h"
 #include "moda_packed.cuh"
 #include "sm100.cuh"
@@ -47,6 +49,8 @@ namespace {
 
 constexpr int kTreeThreads = 352;
 constexpr int kTreeCtas = 148;      // one CTA per SM of a B200
+// Packed prompts of fewer pieces than this (of two full tiles) go through this kernel.
+constexpr int kPromptSmall = 74;
 constexpr int kTreeMinShare = 2;    // steps of the smallest share
 constexpr int kTreeRegion = 16384;  // 128 rows x 128 bytes, swizzled
 constexpr float kLog2eTree = 1.4426950408889634f;
@@ -78,16 +82,9 @@ struct TreeArgs {
   int nt;          // tiles (or tile pairs) per KV head
   int rows;        // rows of a workspace slot
   float scale_log2;
-};
-
-struct TreeBars {
-  uint64_t full[10], empty[10], ready[10];  // ring: landed; released; zeroed where needed
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_half[2], p_full[2];
-  uint64_t o_final, o_free;
-  uint64_t drain;
-  uint32_t tmem_base;
-  int abort;
+  // packed prompts (kPrompt): N is the row count of the token axis
+  const int* cu;  // [nseq + 1] first rows of the sequences
+  int nseq, causal;
 };
 
 __device__ __forceinline__ int tree_length(const TreeArgs& a, int b, bool report = false) {
@@ -161,8 +158,9 @@ __device__ __forceinline__ TreePlan tree_plan(const TreeArgs& a) {
 // A CTA's walk over its share: piece by piece, each a run of steps of one item.
 struct TreeWalk {
   long long left;      // steps left behind this piece
-  int b, it;           // sequence and item of it
+  int b, it;           // sequence and item of it (prompts: its first row, the KV head)
   int j0, j1, n, len;  // steps [j0, j1) of n, the sequence's cache length
+  int t0;              // prompts: the item's first token in its sequence
   __device__ __forceinline__ void clip(const TreeArgs& a) {
     len = tree_length(a, b);
     n = a.ND + 1 + (len + 127) / 128;
@@ -182,6 +180,17 @@ struct TreeWalk {
   }
 };
 
+struct TreeBars {
+  uint64_t full[10], empty[10], ready[10];  // ring: landed; released; zeroed where needed
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_half[2], p_full[2];
+  uint64_t o_final, o_free;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  TreeWalk walk;  // this CTA's first piece
+};
+
 // This CTA's first piece (all lanes of a warp); left < 0: there is none.
 __device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, const TreePlan& p) {
   const int lane = threadIdx.x & 31;
@@ -193,6 +202,7 @@ __device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, const TreePlan
   w.b = a.B;
   w.it = 0;
   w.j0 = 0;
+  w.t0 = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int steps = b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0;
     const int mine = p.parts ? p.ctas(steps) : steps;
@@ -259,7 +269,29 @@ __device__ __forceinline__ void ancestor_bits(const int* par, int i, uint32_t (&
   if (p != -1) atomicOr(&g_error_word, kErrInternal);
 }
 
-template <int D, bool kPair>
+// The one item of a CTA in a packed batch of prompts: a tile (or pair) of its sequence's
+// tokens against the depth entries and the key blocks up to its last token.
+__device__ __forceinline__ TreeWalk prompt_item(const TreeArgs& a, int tokens) {
+  TreeWalk w;
+  const PackedPiece pc = packed_find(a.cu, a.nseq, a.N, tokens, int(blockIdx.x) / a.Hkv);
+  w.left = pc.found ? 0 : -1;  // (the grid is sized by an upper bound)
+  w.b = pc.first;
+  w.it = int(blockIdx.x) % a.Hkv;
+  w.len = pc.len;
+  w.t0 = pc.p * tokens;
+  w.j0 = 0;
+  w.j1 = w.n = a.ND + ((a.causal ? min(pc.len, w.t0 + tokens) : pc.len) + 127) / 128;
+  return w;
+}
+
+// Where an item's data lie.
+struct TreeItem {
+  int g, bg;     // KV head; batch index of the tensor maps
+  int tok, key;  // rows of the first query token and of the first key
+  int t0, ntok;  // first token of the item among its sequence's ntok
+};
+
+template <int D, bool kPair, bool kPrompt>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     moda_tree_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
@@ -292,12 +324,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tma_prefetch_desc(maps[lane]);
   }
 
-  const TreeWalk walk0 = tree_first(a, tree_plan(a));
-  if (blockIdx.x == 0 && warp == 0)
-    for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
-  if (walk0.left < 0) return;
-
-  if (threadIdx.x == 0) {
+  // warp 0 finds this CTA's work while others set up the barriers and the tensor memory
+  if (warp == 0) {
+    TreeWalk w;
+    if constexpr (kPrompt) {
+      w = prompt_item(a, a.TQ * Cfg::kQTiles);
+    } else {
+      w = tree_first(a, tree_plan(a));
+      if (blockIdx.x == 0)
+        for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
+    }
+    if (lane == 0) bars->walk = w;
+  }
+  if (threadIdx.x == 32) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar(bars->full[s]), 1);
       mbar_init(bar(bars->empty[s]), 2);  // the products that read it, and warp 10
@@ -326,6 +365,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  const TreeWalk walk0 = bars->walk;
+  if (walk0.left < 0) {  // no work for this CTA
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    return;
+  }
+  constexpr int kOwn = kPrompt ? 0 : 1;  // steps of the new tokens' own keys
+  auto item_of = [&](const TreeWalk& w) {
+    TreeItem t;
+    if constexpr (kPrompt) {
+      t = TreeItem{w.it, w.it, w.b + w.t0, w.b, w.t0, w.len};
+    } else {
+      const int g = w.it / a.nt, t0 = (w.it - g * a.nt) * a.TQ * Cfg::kQTiles;
+      t = TreeItem{g, w.b * a.Hkv + g, t0, 0, t0, a.N};
+    }
+    return t;
+  };
 
   // Ring entries of a step: keys then values; a depth step of a tile pair has both tiles'
   // keys, then both tiles' values.
@@ -338,9 +393,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       TreeWalk w = walk0;
       bool more = true;
       while (more && !*abort_flag) {
-        const int g = w.it / a.nt, tile = w.it - g * a.nt;
-        const int bg = w.b * a.Hkv + g;
-        const int tok0 = tile * a.TQ * Cfg::kQTiles;
+        const TreeItem item = item_of(w);
         for (int j = w.j0; j < w.j1; ++j) {
           const int ne = wide(j) ? 4 : 2;
           bool ok = true;
@@ -356,14 +409,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               mbar_expect_tx(full, uint32_t(Cfg::kRegions) * 128u * a.TQ * a.JC);
               for (int rg = 0; rg < Cfg::kRegions; ++rg)
                 tma_load_4d(sKV(s) + rg * kTreeRegion, values ? &tmVD : &tmKD, full, rg * 64,
-                            j * a.JC, tok0 + (ne == 4 && (u & 1) ? a.TQ : 0), bg);
+                            j * a.JC, item.tok + (ne == 4 && (u & 1) ? a.TQ : 0), item.bg);
             } else {
               mbar_expect_tx(full, Cfg::kTile);
-              const bool tree = j == a.ND;
+              const bool tree = !kPrompt && j == a.ND;
               const CUtensorMap* map = tree ? (values ? &tmVT : &tmKT) : (values ? &tmV : &tmK);
               for (int rg = 0; rg < Cfg::kRegions; ++rg)
                 tma_load_3d(sKV(s) + rg * kTreeRegion, map, full, rg * 64,
-                            tree ? 0 : (j - a.ND - 1) * 128, bg);
+                            tree ? 0 : item.key + (j - a.ND - kOwn) * 128, item.bg);
             }
           }
           if (!ok) break;
@@ -379,13 +432,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       bool more = true;
       for (; more; ++pc, more = w.next(a)) {
         if (pc > 0 && !mbar_wait(bar(bars->q_empty), (pc - 1) & 1, abort_flag)) break;
-        const int g = w.it / a.nt, tile = w.it - g * a.nt;
+        const TreeItem item = item_of(w);
         mbar_expect_tx(bar(bars->q_full),
                        uint32_t(Cfg::kQTiles * Cfg::kRegions) * 128u * a.G * a.TQ);
         for (int t = 0; t < Cfg::kQTiles; ++t)
           for (int rg = 0; rg < Cfg::kRegions; ++rg)
             tma_load_4d(sQ(t) + rg * kTreeRegion, &tmQ, bar(bars->q_full), rg * 64, 0,
-                        (tile * Cfg::kQTiles + t) * a.TQ, w.b * a.Hkv + g);
+                        item.tok + t * a.TQ, item.bg);
       }
       if (*abort_flag && pc > 0) mbar_wait_drain(bar(bars->q_full), (pc - 1) & 1);
     }
@@ -493,9 +546,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeWalk w = walk0;
     bool more = true, stop = false;
     while (more && !stop) {
-      const int tile = w.it % a.nt;
-      const int tok0 = tile * a.TQ * Cfg::kQTiles;
-      const int* par = a.parents + (long long)w.b * a.N;
+      const TreeItem item = item_of(w);
+      const int* par = kPrompt ? nullptr : a.parents + (long long)w.b * a.N;
       for (int j = w.j0; j < w.j1 && !stop; ++j) {
         const int ne = wide(j) ? 4 : 2;
         for (int u = 0; u < ne; ++u, ++e) {
@@ -504,14 +556,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (stop) break;
           if (ne == 4 ? u >= 2 : u == 1) {
             if (j < a.ND) {
-              // rows that no entry fills, and the entries of unused slots
-              const int t0 = tok0 + (ne == 4 && (u & 1) ? a.TQ : 0);
-              zero_tile_rows(sKV(s), Cfg::kRegions, a.TQ * a.JC, 128);
-              zero_unused(sKV(s), par, t0, min(t0 + a.TQ, a.N), a.JC);
-            } else if (j == a.ND) {
+              // rows that no entry of a token fills, and the entries of unused slots
+              const int t0 = item.t0 + (ne == 4 && (u & 1) ? a.TQ : 0);
+              const int toks = min(a.TQ, max(0, item.ntok - t0));
+              zero_tile_rows(sKV(s), Cfg::kRegions, toks * a.JC, 128);
+              if constexpr (!kPrompt) zero_unused(sKV(s), par, t0, t0 + toks, a.JC);
+            } else if (!kPrompt && j == a.ND) {
               zero_unused(sKV(s), par, 0, a.N, 1);
             } else {
-              const int inside = w.len - (j - a.ND - 1) * 128;
+              const int inside = w.len - (j - a.ND - kOwn) * 128;
               if (inside < 128) zero_tile_rows(sKV(s), Cfg::kRegions, inside, 128);
             }
           }
@@ -603,16 +656,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // Any other step: 32 keys at a time, those no row of the warp sees skipped.  P's columns of
     // a chunk overwrite S columns that were read before.
     auto masked_step = [&](const TreeWalk& w, int j, int ti, const int* par) {
+      (void)par;
       uint32_t vis[4];
       if (j < a.ND) {
         const int lo = tok * a.JC, nv = min(a.JC, a.L - j * a.JC);
 #pragma unroll
         for (int q = 0; q < 4; ++q) vis[q] = range_bits(lo, lo + nv, q);
-      } else if (j == a.ND) {
+      } else if (!kPrompt && j == a.ND) {
         vis[0] = vis[1] = vis[2] = vis[3] = 0u;
         if (tok < a.TQ && ti < a.N) ancestor_bits(par, ti, vis);
       } else {
-        const int inside = w.len - (j - a.ND - 1) * 128;
+        // keys of the block inside the sequence, and of a prompt (causal) up to the token
+        const int end = kPrompt && a.causal ? min(ti + 1, w.len) : w.len;
+        const int inside = end - (j - a.ND - kOwn) * 128;
 #pragma unroll
         for (int q = 0; q < 4; ++q) vis[q] = range_bits(0, inside, q);
       }
@@ -668,13 +724,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // (no early way out: the warpgroups meet at named barriers; once a wait has failed every
     // later one returns at once)
     for (; more; ++pc) {
-      const int g = w.it / a.nt, tile = w.it - g * a.nt;
-      const int t0 = (tile * Cfg::kQTiles + (kPair ? wg : 0)) * a.TQ;
-      const int ti = t0 + tok;  // this row's new token
-      const int* par = a.parents + (long long)w.b * a.N;
-      const bool valid = tok < a.TQ && ti < a.N;
+      const TreeItem item = item_of(w);
+      const int t0 = item.t0 + (kPair ? wg * a.TQ : 0);
+      const int ti = t0 + tok;  // this row's token
+      const int* par = kPrompt ? nullptr : a.parents + (long long)w.b * a.N;
+      const bool valid = tok < a.TQ && ti < item.ntok;
       // warps without a row in the tile only keep the barriers in step
-      const bool active = (warp & 3) * 32 < min(a.TQ, a.N - t0) * a.G;
+      const bool active = (warp & 3) * 32 < min(a.TQ, item.ntok - t0) * a.G;
+      // keys that every row of the tile sees
+      const int sure = kPrompt && a.causal ? min(t0 + 1, w.len) : w.len;
       m = -INFINITY;
       l = 0.f;
       has_o = false;
@@ -684,8 +742,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_wait(bar(bars->s_full[wg]), (unit >> 1) & 1, abort_flag);
         tc_fence_after();
         if (active) {
-          const int kbase = (j - a.ND - 1) * 128;
-          if (j > a.ND && kbase + 128 <= w.len)
+          const int kbase = (j - a.ND - kOwn) * 128;
+          if (j >= a.ND + kOwn && kbase + 128 <= sure)
             full_step();
           else
             masked_step(w, j, ti, par);
@@ -702,7 +760,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int units = (w.j1 - w.j0) * Cfg::kQTiles;
       mbar_wait(bar(bars->o_final), pc & 1, abort_flag);
       tc_fence_after();
-      const bool whole = w.j0 == 0 && w.j1 == w.n;
+      const bool whole = kPrompt || (w.j0 == 0 && w.j1 == w.n);
       float m_all = m, l_all = l, f0 = 1.f, f1 = 0.f;
       constexpr int kCols = kPair ? D : D / 2;  // columns this thread writes
       const int col0 = kPair ? 0 : wg * kCols;
@@ -721,11 +779,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool use0 = kPair || units > 1 || (u & 1) == 0;
       const bool use1 = !kPair && (units > 1 || (u & 1) == 1);
       if (active) {
-        const bool dead = valid && __ldg(par + ti) == -2;  // unused slot: zeros, -inf
+        // an unused slot: zeros, -inf
+        bool dead = false;
+        if constexpr (!kPrompt) dead = valid && __ldg(par + ti) == -2;
         // (l = 0 only for a row that saw nothing)
         const float inv = whole ? ((dead || l_all == 0.f) ? 0.f : 1.f / l_all) : 1.f;
         const long long row =
-            ((long long)w.b * a.Hq + g * a.G + hl) * a.N + (valid ? ti : 0);
+            ((long long)(kPrompt ? 0 : w.b) * a.Hq + item.g * a.G + hl) * a.N +
+            (kPrompt ? item.key : 0) + (valid ? ti : 0);
         // a cut item's first piece in a CTA's share has the share's first slot
         const int slot = 2 * int(blockIdx.x) + (pc > 0 ? 1 : 0);
         const long long wrow = (long long)slot * a.rows + (kPair ? wg * a.TQ * a.G : 0) + r;
@@ -887,7 +948,7 @@ TreeGeom tree_geom(int N, int G, int L) {
   return t;
 }
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kPrompt>
 cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeArgs& a,
                           const void* q, const void* k, const void* v, const void* kt,
                           const void* vt, const void* kd, const void* vd, EncodeTiledFn encode,
@@ -917,7 +978,13 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
     const cuuint32_t box[3] = {64, 128, 1};
     return map(m, base, 3, dims, str, box);
   };
-  ok = ok && keys(&mK, k, p.S) && keys(&mV, v, p.S) && keys(&mKT, kt, p.N) && keys(&mVT, vt, p.N);
+  ok = ok && keys(&mK, k, p.S) && keys(&mV, v, p.S);
+  if (kPrompt) {
+    mKT = mK;  // never loaded
+    mVT = mV;
+  } else {
+    ok = ok && keys(&mKT, kt, p.N) && keys(&mVT, vt, p.N);
+  }
   mKD = mK;  // never loaded when L == 0
   mVD = mV;
   if (p.L > 0) {
@@ -931,20 +998,24 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
     *why = "cuTensorMapEncodeTiled failed for the tree attention's tensors";
     return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(moda_tree_kernel<D, kPair>,
+  cudaError_t e = cudaFuncSetAttribute(moda_tree_kernel<D, kPair, kPrompt>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg::kSmemBytes);
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
     return e;
   }
-  moda_tree_kernel<D, kPair><<<kTreeCtas, kTreeThreads, Cfg::kSmemBytes, stream>>>(
+  const unsigned grid =
+      kPrompt ? unsigned(p.Hkv * packed_pieces_bound(p.N, a.nseq, tg.TQ * Cfg::kQTiles))
+              : unsigned(kTreeCtas);
+  moda_tree_kernel<D, kPair, kPrompt><<<grid, kTreeThreads, Cfg::kSmemBytes, stream>>>(
       mQ, mK, mV, mKT, mVT, mKD, mVD, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) {
-    *why = "tree attention launch failed";
+    *why = kPrompt ? "packed forward launch failed" : "tree attention launch failed";
     return e;
   }
+  if (kPrompt) return e;
   // programmatic dependent launch: see the decode's combine step
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(((long long)p.B * p.Hq * p.N + 7) / 8));
@@ -961,6 +1032,27 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
   return e;
 }
 
+TreeArgs tree_args(const TreeProblem& p, const TreeGeom& t, void* out, float* lse) {
+  TreeArgs a = {};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.B = p.B;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = p.Hq / p.Hkv;
+  a.N = p.N;
+  a.S = p.S;
+  a.L = p.L;
+  a.TQ = t.TQ;
+  a.JC = t.JC;
+  a.ND = t.ND;
+  a.nt = t.nt;
+  a.nit = p.Hkv * t.nt;
+  a.rows = t.rows;
+  a.scale_log2 = p.scale * kLog2eTree;
+  return a;
+}
+
 }  // namespace
 
 size_t tree_workspace_bytes(const TreeProblem& p) {
@@ -973,35 +1065,63 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
                         const int* parents, const int* lengths, void* out, float* lse,
                         void* workspace, EncodeTiledFn encode, cudaStream_t stream,
                         const char** why) {
-  const int G = p.Hq / p.Hkv;
-  const TreeGeom t = tree_geom(p.N, G, p.L);
-  TreeArgs a;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.lse = lse;
+  const TreeGeom t = tree_geom(p.N, p.Hq / p.Hkv, p.L);
+  TreeArgs a = tree_args(p, t, out, lse);
   a.ws_acc = static_cast<float*>(workspace);
   a.ws_ml = a.ws_acc + size_t(2 * kTreeCtas) * t.rows * p.d;
   a.parents = parents;
   a.lengths = lengths;
-  a.B = p.B;
-  a.Hq = p.Hq;
-  a.Hkv = p.Hkv;
-  a.G = G;
-  a.N = p.N;
-  a.S = p.S;
-  a.L = p.L;
-  a.TQ = t.TQ;
-  a.JC = t.JC;
-  a.ND = t.ND;
-  a.nt = t.nt;
-  a.nit = p.Hkv * t.nt;
-  a.rows = t.rows;
-  a.scale_log2 = p.scale * kLog2eTree;
+  auto go = [&](auto d_c, auto pair_c) {
+    return launch_tree_d<decltype(d_c)::value, decltype(pair_c)::value, false>(
+        p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why);
+  };
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
   if (p.d == 128)
-    return t.pair ? launch_tree_d<128, true>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why)
-                  : launch_tree_d<128, false>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
-                                              why);
-  return t.pair ? launch_tree_d<64, true>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why)
-                : launch_tree_d<64, false>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream, why);
+    return t.pair ? go(D128{}, std::true_type{}) : go(D128{}, std::false_type{});
+  return t.pair ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
+}
+
+PromptTile prompt_tile(const Problem& p) {
+  const int full = 128 / p.G;
+  // pieces of a size, about: each sequence ends in a piece that is half full
+  auto pieces = [&](int tokens) {
+    return p.Hkv * ((long long)p.T / tokens + (p.nseq < p.T ? p.nseq : p.T) / 2);
+  };
+  if (pieces(2 * full) > kPromptSmall) {
+    // the forward kernel, unless the group has no dense depth path there
+    if (p.L == 0 || dense_depth_supported(p)) return PromptTile{0, false};
+    return PromptTile{full, true};
+  }
+  int tokens = full;
+  while (tokens > 1 && pieces(tokens / 2) <= kTreeCtas) tokens /= 2;
+  return PromptTile{tokens, false};
+}
+
+cudaError_t launch_prompt(const Problem& p, const PromptTile& tile, const void* q, const void* k,
+                          const void* v, const void* kd, const void* vd, void* out, float* lse,
+                          EncodeTiledFn encode, cudaStream_t stream, const char** why) {
+  const TreeProblem tp{1, p.Hq, p.Hkv, p.T, p.T, p.L, p.d, p.scale};
+  TreeGeom t;
+  t.TQ = tile.tokens;
+  t.JC = 128 / t.TQ;
+  t.ND = (p.L + t.JC - 1) / t.JC;
+  t.pair = tile.pair;
+  t.tiles = t.nt = 1;
+  t.rows = 0;  // (no workspace)
+  TreeArgs a = tree_args(tp, t, out, lse);
+  a.cu = p.cu;
+  a.nseq = p.nseq;
+  a.causal = p.causal;
+  auto go = [&](auto d_c, auto pair_c) {
+    return launch_tree_d<decltype(d_c)::value, decltype(pair_c)::value, true>(
+        tp, t, a, q, k, v, nullptr, nullptr, kd, vd, encode, stream, why);
+  };
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
+  if (p.d == 128)
+    return t.pair ? go(D128{}, std::true_type{}) : go(D128{}, std::false_type{});
+  return t.pair ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
 }
 
 }  // namespace moda

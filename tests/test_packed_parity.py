@@ -34,6 +34,19 @@ CASES = [
     ("full-d64", [129, 1, 260], 0, 3, 4, 2, 64, 0, False),
     ("full-g3", [50, 130], 3, 0, 6, 2, 128, 2, False),
     ("one-sequence", [1000], 0, 0, 8, 2, 128, 6, True),
+    # enough tokens for the forward's own kernel (the ones above run on the tree attention's)
+    ("big-g4-d128", [1300, 0, 1, 700, 129, 64, 127, 500], 3, 5, 8, 2, 128, 5, True),
+    ("big-g4-d128-L0", [900, 31, 33, 1700, 255], 1, 2, 8, 2, 128, 0, True),
+    ("big-g1-d64", [1100, 129, 128, 127, 1300, 260], 0, 7, 8, 8, 64, 3, True),
+    ("big-g2-d64", [700, 1, 900, 65, 63], 2, 0, 8, 4, 64, 9, True),
+    ("big-g16-d128", [500, 8, 9, 700], 0, 3, 16, 1, 128, 18, True),
+    ("big-g32-d64", [300, 5, 400], 1, 1, 32, 1, 64, 33, True),
+    ("big-g3-d128", [1200, 83, 85, 84, 1900, 0, 43], 2, 9, 6, 2, 128, 4, True),
+    ("big-g3-d64-L0", [1700, 84, 1500], 0, 5, 6, 2, 64, 0, True),
+    ("big-g64-d64", [100, 3, 200], 1, 1, 64, 1, 64, 5, True),
+    ("big-full-g4", [700, 129, 1500, 1], 4, 3, 8, 2, 128, 5, False),
+    ("big-full-g3", [1500, 90, 1700], 0, 3, 6, 2, 64, 3, False),
+    ("big-many", [(13 * i) % 61 for i in range(100)], 2, 2, 16, 4, 128, 4, True),
 ]
 IDS = [c[0] for c in CASES]
 
@@ -119,8 +132,8 @@ def test_backward_packed(case):
 
 @pytest.mark.parametrize("causal", [True, False])
 def test_each_sequence_equals_its_own_forward(causal):
-    # the same kernel over the same blocks: every bit agrees with moda_forward's
-    case = ("bits", [300, 64, 1, 129], 0, 5, 8, 2, 128, 6, causal)
+    # the forward's kernel over the same blocks: every bit agrees with moda_forward's
+    case = ("bits", [3000, 64, 1, 1290], 0, 5, 8, 2, 128, 6, causal)
     x, ends = make(case, 31)
     out, lse = moda.forward_packed(x["q"], x["k"], x["v"], x["cu"], x["kd"], x["vd"],
                                    causal=causal)
@@ -131,10 +144,12 @@ def test_each_sequence_equals_its_own_forward(causal):
     moda.check_device_errors()
 
 
+@pytest.mark.parametrize("G", [3, 4])
+@pytest.mark.parametrize("times", [1, 40])
 @pytest.mark.parametrize("d", [64, 128])
-def test_a_neighbours_infinities_stay_with_it(d):
+def test_a_neighbours_infinities_stay_with_it(d, times, G):
     # one sequence full of NaN and infinities between two others, in every input
-    case = ("neighbours", [45, 50, 75], 0, 0, 8, 2, d, 3, True)
+    case = ("neighbours", [45 * times, 50 * times, 75], 0, 0, 2 * G, 2, d, 3, True)
     x, ends = make(case, 77, dout=True)
     args = [x[n] for n in ("q", "k", "v", "cu", "kd", "vd")]
     out, lse = moda.forward_packed(*args)
