@@ -610,15 +610,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (lane == 0) mbar_arrive(bar(b));
     };
     // P enters its product as bf16 (the products' operand type); l sums it unrounded.
-    // A cache block that lies inside the cache: no mask, every fourth pair of exponentials on
-    // the FMA pipe, as in the forward.
-    auto full_step = [&]() {
+    // All 128 keys of a step.  Without a mask (a block inside the cache) every fourth pair of
+    // exponentials is computed on the FMA pipe, as in the forward.
+    auto full_step = [&](auto masked_c, const uint32_t (&vis)[4]) {
+      constexpr bool kMasked = decltype(masked_c)::value;
       uint32_t s[128];
       tmem_ld32(tS + 0, &s[0]);
       tmem_ld32(tS + 32, &s[32]);
       tmem_ld32(tS + 64, &s[64]);
       tmem_ld32(tS + 96, &s[96]);
       tmem_wait_ld();
+      if constexpr (kMasked) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+      }
       float mx = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 128; c += 4) {
@@ -628,9 +634,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const float m_cand = fmaxf(m, fmaxf(mx, mx1) * a.scale_log2);
       const bool grow = m_cand > m + kTreeRescale;
       const float m_new = grow ? m_cand : m;
-      const float alpha = ex2(m - m_new);
+      const float m_use = kMasked && m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = ex2(m - m_use);
       const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-      const float2 nm2 = make_float2(-m_new, -m_new);
+      const float2 nm2 = make_float2(-m_use, -m_use);
       float2 ps = make_float2(0.f, 0.f);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float2 x = ffma2(make_float2(__uint_as_float(s[half * 64 + c]),
                                              __uint_as_float(s[half * 64 + c + 1])),
                                  sl2, nm2);
-          const float2 p = (c / 2) % kExpFmaPeriod == kExpFmaPeriod - 1
+          const float2 p = !kMasked && (c / 2) % kExpFmaPeriod == kExpFmaPeriod - 1
                                ? exp2_fma2(x)
                                : make_float2(ex2(x.x), ex2(x.y));
           ps = fadd2(ps, p);
@@ -653,8 +660,66 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       l = l * alpha + (ps.x + ps.y);
       m = m_new;
     };
-    // Any other step: 32 keys at a time, those no row of the warp sees skipped.  P's columns of
-    // a chunk overwrite S columns that were read before.
+    // Keys of kW chunks of 32 from chunk q0 on (0 <= q0 <= 4 - kW), the only ones that some row
+    // of the warp sees; P is zero elsewhere.
+    auto window_step = [&](auto width_c, int q0, const uint32_t (&vis)[4]) {
+      constexpr int kW = decltype(width_c)::value;
+      uint32_t see[kW];
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        const int q = q0 + i;
+        see[i] = q < 2 ? (q ? vis[1] : vis[0]) : (q > 2 ? vis[3] : vis[2]);
+      }
+      uint32_t s[32 * kW];
+#pragma unroll
+      for (int i = 0; i < kW; ++i) tmem_ld32(tS + 32 * (q0 + i), &s[32 * i]);
+      tmem_wait_ld();
+      float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32 * kW; ++c)
+        if (!((see[c / 32] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+#pragma unroll
+      for (int c = 0; c < 32 * kW; c += 4) {
+        mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+      }
+      const float m_cand = fmaxf(m, fmaxf(mx, mx1) * a.scale_log2);
+      const bool grow = m_cand > m + kTreeRescale;
+      const float m_new = grow ? m_cand : m;
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = ex2(m - m_use);
+      const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+      const float2 nm2 = make_float2(-m_use, -m_use);
+      float2 ps = make_float2(0.f, 0.f);
+      uint32_t pk[16 * kW];
+#pragma unroll
+      for (int c = 0; c < 32 * kW; c += 2) {
+        const float2 x =
+            ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, nm2);
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+        ps = fadd2(ps, p);
+        pk[c / 2] = pack_bf16x2(p.x, p.y);
+      }
+      rescale_o(grow, alpha);
+      uint32_t zero[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) zero[c] = 0u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q < q0 || q >= q0 + kW)
+          tmem_st16(tS + 16 * q, zero);
+        else if (kW == 1 || q == q0)
+          tmem_st16(tS + 16 * q, &pk[0]);
+        else
+          tmem_st16(tS + 16 * q, &pk[16 * (kW - 1)]);
+        if (q & 1) publish(q == 3 ? bars->p_full[wg] : bars->p_half[wg]);
+      }
+      l = l * alpha + (ps.x + ps.y);
+      m = m_new;
+    };
+    // Any other step.  Most let a warp's rows see only keys inside 32 or 64 columns (a token's
+    // depth entries, a small tree, the edge of a block): those alone are loaded and
+    // exponentiated.
     auto masked_step = [&](const TreeWalk& w, int j, int ti, const int* par) {
       (void)par;
       uint32_t vis[4];
@@ -672,51 +737,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) vis[q] = range_bits(0, inside, q);
       }
-      float mx = -INFINITY;
+      int q0 = 4, q1 = 0;  // chunks of 32 keys [q0, q1) hold all that the warp's rows see
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (!__any_sync(0xffffffffu, vis[q] != 0u)) continue;
-        uint32_t s[32];
-        tmem_ld32(tS + 32 * q, s);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if ((vis[q] >> c) & 1u) mx = fmaxf(mx, __uint_as_float(s[c]));
-      }
-      const float m_cand = fmaxf(m, mx * a.scale_log2);
-      const bool grow = m_cand > m + kTreeRescale;
-      const float m_new = grow ? m_cand : m;
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = ex2(m - m_use);
-      float ps = 0.f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
+      for (int q = 0; q < 4; ++q)
         if (__any_sync(0xffffffffu, vis[q] != 0u)) {
-          uint32_t s[32];
-          tmem_ld32(tS + 32 * q, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float x0 = fmaf(__uint_as_float(s[c]), a.scale_log2, -m_use);
-            const float x1 = fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -m_use);
-            const float p0 = ex2((vis[q] >> c) & 1u ? x0 : -INFINITY);
-            const float p1 = ex2((vis[q] >> c) & 2u ? x1 : -INFINITY);
-            ps += p0 + p1;
-            pk[c / 2] = pack_bf16x2(p0, p1);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = 0u;
+          q0 = min(q0, q);
+          q1 = q + 1;
         }
-        if (q == 0) rescale_o(grow, alpha);
-        tmem_st16(tS + 16 * q, pk);
-        if (q == 1) publish(bars->p_half[wg]);
-        if (q == 3) publish(bars->p_full[wg]);
+      if (q1 - q0 > 2) {
+        full_step(std::true_type{}, vis);
+        return;
       }
-      l = l * alpha + ps;
-      m = m_new;
+      if (q1 - q0 == 2)
+        window_step(std::integral_constant<int, 2>{}, q0, vis);
+      else
+        window_step(std::integral_constant<int, 1>{}, min(q0, 3), vis);
     };
+    const uint32_t no_mask[4] = {0u, 0u, 0u, 0u};
     TreeWalk w = walk0;
     int u = 0;  // unit
     int pc = 0;
@@ -744,7 +781,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (active) {
           const int kbase = (j - a.ND - kOwn) * 128;
           if (j >= a.ND + kOwn && kbase + 128 <= sure)
-            full_step();
+            full_step(std::false_type{}, no_mask);
           else
             masked_step(w, j, ti, par);
         } else {
