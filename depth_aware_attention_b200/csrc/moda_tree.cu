@@ -49,8 +49,6 @@ namespace {
 
 constexpr int kTreeThreads = 352;
 constexpr int kTreeCtas = 148;      // one CTA per SM of a B200
-// Packed prompts of fewer pieces than this (of two full tiles) go through this kernel.
-constexpr int kPromptSmall = 74;
 constexpr int kTreeMinShare = 2;    // steps of the smallest share
 constexpr int kTreeRegion = 16384;  // 128 rows x 128 bytes, swizzled
 constexpr float kLog2eTree = 1.4426950408889634f;
@@ -1119,17 +1117,23 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
   return t.pair ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
 }
 
+// The forward kernel's pairs of tiles make better use of the tensor cores, single tiles (whose
+// two warpgroups take alternate key blocks) are done sooner.  So single tiles are taken while
+// their CTAs fit the GPU at once, smaller ones as long as that still holds: with few tokens a
+// tile, a depth step holds more of each token's entries.  (16 heads in groups of 4, d = 128,
+// L = 24: 411 tokens 13.1 us against the forward kernel's 21.3; 2000 tokens 42 against 40.)
+// Groups without a dense depth path in the forward kernel run here at any size, in pairs once
+// the pairs fill the GPU (groups of 3, d = 64, L = 7: 5000 tokens, 120 pairs, 27 us in single
+// tiles and 31 in pairs; 9000 tokens, 210 pairs, 50 and 41).
 PromptTile prompt_tile(const Problem& p) {
   const int full = 128 / p.G;
   // pieces of a size, about: each sequence ends in a piece that is half full
   auto pieces = [&](int tokens) {
     return p.Hkv * ((long long)p.T / tokens + (p.nseq < p.T ? p.nseq : p.T) / 2);
   };
-  if (pieces(2 * full) > kPromptSmall) {
-    // the forward kernel, unless the group has no dense depth path there
-    if (p.L == 0 || dense_depth_supported(p)) return PromptTile{0, false};
-    return PromptTile{full, true};
-  }
+  const bool dense = p.L == 0 || dense_depth_supported(p);
+  if (pieces(dense ? full : 2 * full) > kTreeCtas)
+    return dense ? PromptTile{0, false} : PromptTile{full, true};
   int tokens = full;
   while (tokens > 1 && pieces(tokens / 2) <= kTreeCtas) tokens /= 2;
   return PromptTile{tokens, false};
