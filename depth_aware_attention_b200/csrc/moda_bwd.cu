@@ -674,6 +674,9 @@ struct SeqCfg {
   static constexpr int kOffLD = kOffDS + 2 * kBwdRegion;  // [2 stages][lse2 | D][128] f32
   static constexpr int kOffBar = kOffLD + 2 * 2 * 128 * 4;
   static constexpr int kSmemBytes = kOffBar + 256;
+  // packed, d = 64: dQ's staging buffer, two 128-row regions of 32 fp32 columns
+  static constexpr int kOffStage = (kSmemBytes + 1023) / 1024 * 1024;
+  static constexpr int kSmemPacked = kOffStage + 2 * kBwdRegion;
 };
 
 struct SeqBars {
@@ -739,8 +742,13 @@ __device__ __forceinline__ void own_tile_rows(const SeqArgs& a, const SeqSpan& w
   r1 = min(a.TQ, w.row1 - t0) * a.G;
 }
 
+// Packed batches are short walks, where the time of one tile counts: there the P/dS work of a
+// tile is shared by two groups of four warps (0-3 rows [0, 64), 12-15 rows [64, 128)), and dQ
+// has TMEM columns and a staging buffer of its own, so that the next tile's S^T and dP^T need
+// not wait for its readout.  (11 sequences of 2003 tokens, 6 heads: 61 us with the other order.)
+constexpr int kSeqPackedThreads = 512;
 template <int D, bool kPacked>
-__global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
+__global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
     moda_bwd_seq_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmDO,
                         const __grid_constant__ CUtensorMap tmK,
@@ -785,7 +793,7 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
     if (kPacked) mbar_init(bar(bars->kv_clean), 1);
     mbar_init(bar(bars->s_full), 1);
     mbar_init(bar(bars->dp_full), 1);
-    mbar_init(bar(bars->pds_full), 128);
+    mbar_init(bar(bars->pds_full), kPacked ? 256 : 128);
     mbar_init(bar(bars->dq_full), 1);
     mbar_init(bar(bars->dq_free), 128);
     mbar_init(bar(bars->kv_done), 1);
@@ -816,6 +824,10 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
   // dK [256+D, 256+2D).  P^T and dS^T are stored as bf16 hi/lo pairs: each 32-row chunk
   // occupies 32 columns, 16 of packed hi values then 16 of packed lo values.
   const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+  // dQ: over S^T, or (packed) in columns of its own, staged behind the barriers
+  static_assert(!kPacked || 256 + 3 * D <= 512, "no room for dQ");
+  const uint32_t tDQ = kPacked ? tmem + 256 + 2 * D : tS;
+  const uint32_t sStage = kPacked ? s0 + Cfg::kOffStage : sDS;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -903,11 +915,15 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
           mma_ts(tDV, tS + col + 16, bd, idesc_g, 1u);
         }
         tc_commit(bar(bars->do_empty[st]));
-        // dQ = dS K into the S^T columns : A = dS (rows x keys, MN-major in shared memory),
-        // B = K (keys x D)
+        if constexpr (kPacked) {
+          if (i + 1 < ntiles) issue_s(i + 1);  // over P^T, which dV has read
+          if (i > 0) mbar_wait(bar(bars->dq_free), (i - 1) & 1, abort_flag);
+          tc_fence_after();
+        }
+        // dQ = dS K : A = dS (rows x keys, MN-major in shared memory), B = K (keys x D)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ss(tS, make_sdesc_sw128(sDS + ks * 2048, kBwdRegion, 1024),
+          mma_ss(tDQ, make_sdesc_sw128(sDS + ks * 2048, kBwdRegion, 1024),
                  make_sdesc_sw128(sK + ks * 2048, kBwdRegion, 1024), idesc_q, ks > 0 ? 1u : 0u);
         tc_commit(bar(bars->dq_full));
         // dK += dS^T Q (hi then lo)
@@ -920,19 +936,23 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
         }
         tc_commit(bar(bars->q_empty[st]));
         if (i + 1 < ntiles) {
+          // (its commit also tells the P/dS warps that dQ has read dS from shared memory)
           issue_dp(i + 1);
-          mbar_wait(bar(bars->dq_free), i & 1, abort_flag);
-          issue_s(i + 1);
+          if constexpr (!kPacked) {
+            mbar_wait(bar(bars->dq_free), i & 1, abort_flag);
+            issue_s(i + 1);
+          }
         }
       }
       tc_commit(bar(bars->kv_done));
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp < 4 || (kPacked && warp >= 12)) {
     // ------------------------------------------------------------ P / dS warps
-    const int tid = threadIdx.x;  // TMEM lane = key key0 + tid
+    const int tid = threadIdx.x & 127;  // TMEM lane = key key0 + tid
+    const int group = kPacked ? warp >> 3 : 0;  // packed: rows [64 group, 64 group + 64)
     const int key = key0 + tid;
-    const uint32_t lane_base = uint32_t(warp * 32) << 16;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const int hl = tid % a.G, tok = tid / a.G;
     // lse and D of row `tid` of tile i, loaded one tile ahead so the global-load latency
     // stays off the per-tile critical path
@@ -943,15 +963,17 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
       lse2v = valid ? -a.lse[idx] * kLog2eBwd : -INFINITY;  // stored negated
       dv_ = valid ? -a.drow[idx] : 0.f;                      // stored negated
     };
-    float nxt_lse, nxt_d;
-    load_rowterms(0, nxt_lse, nxt_d);
+    float nxt_lse = 0.f, nxt_d = 0.f;
+    if (group == 0) load_rowterms(0, nxt_lse, nxt_d);
     for (int i = 0; i < ntiles; ++i) {
       const int qt = first_qt + i;
       const int b = i & 1;
-      ld_s[b * 256 + tid] = nxt_lse;
-      ld_s[b * 256 + 128 + tid] = nxt_d;
-      named_bar_sync(1, 128);
-      load_rowterms(i + 1, nxt_lse, nxt_d);
+      if (group == 0) {
+        ld_s[b * 256 + tid] = nxt_lse;
+        ld_s[b * 256 + 128 + tid] = nxt_d;
+      }
+      named_bar_sync(1, kPacked ? 256 : 128);
+      if (group == 0) load_rowterms(i + 1, nxt_lse, nxt_d);
       // rows r < r_min hold tokens before this key (causal) -- their weight is zero
       int r_min = 0;
       if (key >= row1)
@@ -964,7 +986,7 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
       mbar_wait(bar(bars->dp_full), i & 1, abort_flag);
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 2 * group; c < (kPacked ? 2 * group + 2 : 4); ++c) {
         uint32_t s[32], dp[32];
         tmem_ld32(tS + lane_base + c * 32, s);
         tmem_ld32(tDP + lane_base + c * 32, dp);
@@ -1026,7 +1048,7 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
     const bool kvalid = key < row1;
     const long long koff = ((long long)bg * a.T + (kvalid ? key : 0)) * D;
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
+    for (int which = group; which < (kPacked ? group + 1 : 2); ++which) {
       const uint32_t tsrc = (which ? tDK : tDV) + lane_base;
       __nv_bfloat16* dst = (which ? a.dk : a.dv) + koff;
 #pragma unroll
@@ -1046,6 +1068,8 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
         }
       }
     }
+  } else if (kPacked && warp == 11) {
+    // (idle: the second P/dS group's warps begin at a multiple of four, as TMEM lanes do)
   } else if (kPacked && warp == 10) {
     // ------------------------------------------------------------ neighbours' rows
     const int lane = threadIdx.x & 31;
@@ -1102,13 +1126,13 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t o[32];
-          tmem_ld32(tS + lane_base + half * 64 + q * 32, o);
+          tmem_ld32(tDQ + lane_base + half * 64 + q * 32, o);
           tmem_wait_ld();
           if (kPacked && !own) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          const uint32_t reg = sDS + q * kBwdRegion + uint32_t(r) * 128;
+          const uint32_t reg = sStage + q * kBwdRegion + uint32_t(r) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             sts128(reg + ((uint32_t(c) ^ (uint32_t(r) & 7u)) << 4),
@@ -1117,8 +1141,8 @@ __global__ void __launch_bounds__(kSeqThreads + (kPacked ? 32 : 0), 1)
         fence_proxy_async_smem();
         named_bar_sync(2, 128);
         if (r == 0) {
-          tma_reduce_add_4d(&tmDQ, sDS, half * 64, 0, t0q, bg);
-          tma_reduce_add_4d(&tmDQ, sDS + kBwdRegion, half * 64 + 32, 0, t0q, bg);
+          tma_reduce_add_4d(&tmDQ, sStage, half * 64, 0, t0q, bg);
+          tma_reduce_add_4d(&tmDQ, sStage + kBwdRegion, half * 64 + 32, 0, t0q, bg);
           bulk_commit_group();
           bulk_wait_read_all();
         }
@@ -1960,20 +1984,18 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
         *why = "cuTensorMapEncodeTiled failed for the dq accumulator";
         return cudaErrorInvalidValue;
       }
-      auto run = [&](auto kernel, int threads) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SeqCfg<D>::kSmemBytes);
+      auto run = [&](auto kernel, int threads, int smem) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) {
           *why = "cudaFuncSetAttribute(sequence backward) failed";
           return;
         }
-        kernel<<<unsigned(BG) * nkb, threads, SeqCfg<D>::kSmemBytes, stream>>>(mQ, mDO, mK, mV,
-                                                                               mDQ, sa);
+        kernel<<<unsigned(BG) * nkb, threads, smem, stream>>>(mQ, mDO, mK, mV, mDQ, sa);
       };
       if (p.cu)
-        run(moda_bwd_seq_kernel<D, true>, kSeqThreads + 32);
+        run(moda_bwd_seq_kernel<D, true>, kSeqPackedThreads, SeqCfg<D>::kSmemPacked);
       else
-        run(moda_bwd_seq_kernel<D, false>, kSeqThreads);
+        run(moda_bwd_seq_kernel<D, false>, kSeqThreads, SeqCfg<D>::kSmemBytes);
       if (e != cudaSuccess) return e;
     }
     e = cudaGetLastError();
