@@ -33,6 +33,7 @@
 // first and the last tile of a walk, and the key block at a sequence's end, may hold rows of
 // a neighbour: one more warp zeroes those rows of Q, dO, K and V before the tensor cores
 // read them, and their row terms are set to weight zero.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -698,6 +699,7 @@ struct SeqArgs {
   float scale, scale_log2;
   const int* cu;  // packed: [nseq + 1] first rows of the sequences (T is the row count N)
   int nseq;
+  int cl;  // packed: CTAs (a cluster) that share one key block's walk
 };
 
 // What one CTA of the sequence kernels owns: keys [key0, min(key0 + 128, row1)) of the
@@ -706,10 +708,14 @@ struct SeqArgs {
 struct SeqSpan {
   int key0, row0, row1, first_qt, ntiles;
   bool head, tail;  // the first / last tile holds rows of a neighbour
+  int bg, rank;     // (batch, KV head); place in the cluster that shares the walk
 };
 template <bool kPacked>
 __device__ __forceinline__ bool seq_span(const SeqArgs& a, SeqSpan& w) {
-  const int kb = blockIdx.x / a.BG;  // key blocks nearest the start see the most tiles
+  const int job = kPacked ? int(blockIdx.x) / a.cl : int(blockIdx.x);
+  w.rank = kPacked ? int(blockIdx.x) - job * a.cl : 0;
+  w.bg = job % a.BG;
+  const int kb = job / a.BG;  // key blocks nearest the start see the most tiles
   if constexpr (kPacked) {
     const PackedPiece pc = packed_find(a.cu, a.nseq, a.T, 128, kb);
     if (!pc.found) return false;  // the grid is sized by an upper bound
@@ -718,6 +724,11 @@ __device__ __forceinline__ bool seq_span(const SeqArgs& a, SeqSpan& w) {
     w.key0 = pc.first + 128 * (pc.n - 1 - pc.p);
     w.first_qt = (a.causal ? w.key0 : w.row0) / a.TQ;
     w.ntiles = (w.row1 - 1) / a.TQ - w.first_qt + 1;
+    if (a.cl > 1) {  // this CTA's part of the walk (it may be empty)
+      const int each = (w.ntiles + a.cl - 1) / a.cl;
+      w.first_qt += w.rank * each;
+      w.ntiles = max(0, min(each, w.ntiles - w.rank * each));
+    }
     w.head = w.first_qt * a.TQ < w.row0;
     w.tail = (w.first_qt + w.ntiles) * a.TQ > w.row1;
   } else {
@@ -730,6 +741,79 @@ __device__ __forceinline__ bool seq_span(const SeqArgs& a, SeqSpan& w) {
   }
   return true;
 }
+// dV and dK of a key block whose walk a cluster of CTAs shared (packed batches): summed in fp32
+// over distributed shared memory, in the order of the ranks halved again and again, and stored
+// by rank 0.  `part`: the calling thread holds row `kt` of dV (which = 0) or dK (1) in TMEM at
+// `acc`; buf: 2 x 128 x D floats in the memory of the Q and dO tiles, which nothing uses any
+// more.  All threads of the cluster call it.
+template <int D>
+__device__ __forceinline__ void join_keys(const SeqArgs& a, const SeqSpan& w, bool part, int which,
+                                          int kt, uint32_t acc, float4* buf) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int key = w.key0 + kt;
+  const long long koff = ((long long)w.bg * a.T + min(key, a.T - 1)) * D;
+  __nv_bfloat16* const dst = (which ? a.dk : a.dv) + koff;
+  bool some = w.ntiles > 0;  // the accumulators hold anything
+  tc_fence_before();
+  cluster.sync();
+  tc_fence_after();
+  for (int h = a.cl >> 1; h >= 1; h >>= 1) {
+    // 16 bytes of column group c of row kt at [which][c][kt]: 512 bytes a warp
+    if (part && w.rank >= h && w.rank < 2 * h) {
+      float4* const to = cluster.map_shared_rank(buf, w.rank - h) + which * (D / 4) * 128 + kt;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(acc + cc * 32, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 x = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                       __uint_as_float(o[4 * q + 2]),
+                                       __uint_as_float(o[4 * q + 3]));
+          to[(cc * 8 + q) * 128] = some ? x : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+    cluster.sync();
+    if (part && w.rank < h) {
+      const float4* const from = buf + which * (D / 4) * 128 + kt;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(acc + cc * 32, o);
+        tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 x = from[(cc * 8 + q) * 128];
+          const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[4 * q + e] = (some ? __uint_as_float(o[4 * q + e]) : 0.f) + y[e];
+        }
+        if (h > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(v[e]);
+          tmem_st32(acc + cc * 32, o);
+        } else if (key < w.row1) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = v[8 * q + e];
+            reinterpret_cast<uint4*>(dst + cc * 32)[q] = pack8(f, 1.f);
+          }
+        }
+      }
+      if (h > 1) tmem_wait_st();
+      some = true;
+    }
+    if (h > 1) cluster.sync();  // (the buffer is written again)
+  }
+}
+
 // Whether tile i of the walk holds rows of a neighbour.
 __device__ __forceinline__ bool mixed_tile(const SeqSpan& w, int i) {
   return (w.head && i == 0) || (w.tail && i == w.ntiles - 1);
@@ -772,9 +856,10 @@ __global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
   const int warp = threadIdx.x >> 5;
-  const int bg = blockIdx.x % a.BG;
   SeqSpan w;
   if (!seq_span<kPacked>(a, w)) return;
+  const int bg = w.bg;
+  const bool shared_walk = kPacked && a.cl > 1;
   const int key0 = w.key0, row1 = w.row1, first_qt = w.first_qt, ntiles = w.ntiles;
   const bool kv_mixed = kPacked && key0 + 128 > row1;  // the key block reaches past the end
 
@@ -899,8 +984,10 @@ __global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
       // Per tile: dV, then dQ into the S^T columns (free once dV has read P^T), then dK,
       // then the next tile's dP^T (its columns are free once dK has read dS^T).  Only
       // the next S^T waits for the dQ readout, which overlaps dK and the next dP^T.
-      issue_s(0);
-      issue_dp(0);
+      if (!kPacked || ntiles > 0) {
+        issue_s(0);
+        issue_dp(0);
+      }
       for (int i = 0; i < ntiles; ++i) {
         const int st = i & 1;
         mbar_wait(bar(bars->pds_full), i & 1, abort_flag);
@@ -1048,7 +1135,7 @@ __global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
     const bool kvalid = key < row1;
     const long long koff = ((long long)bg * a.T + (kvalid ? key : 0)) * D;
 #pragma unroll 1
-    for (int which = group; which < (kPacked ? group + 1 : 2); ++which) {
+    for (int which = group; which < (shared_walk ? 0 : (kPacked ? group + 1 : 2)); ++which) {
       const uint32_t tsrc = (which ? tDK : tDV) + lane_base;
       __nv_bfloat16* dst = (which ? a.dk : a.dv) + koff;
 #pragma unroll
@@ -1152,6 +1239,12 @@ __global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
       mbar_arrive(bar(bars->dq_free));
     }
     if (r == 0) bulk_wait_all();
+  }
+  if (shared_walk) {
+    __syncwarp();
+    join_keys<D>(a, w, warp < 4 || warp >= 12, warp >= 12 ? 1 : 0, int(threadIdx.x & 127),
+                 (warp >= 12 ? tDK : tDV) + (uint32_t((warp & 3) * 32) << 16),
+                 reinterpret_cast<float4*>(smem + Cfg::kOffQ));
   }
 
   tc_fence_before();
@@ -1302,9 +1395,10 @@ __global__ void __launch_bounds__(kSeqHThreads + (kPacked ? 32 : 0), 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
   const int warp = threadIdx.x >> 5;
-  const int bg = blockIdx.x % a.BG;
   SeqSpan w;
   if (!seq_span<kPacked>(a, w)) return;
+  const int bg = w.bg;
+  const bool shared_walk = kPacked && a.cl > 1;
   const int key0 = w.key0, row1 = w.row1, first_qt = w.first_qt, ntiles = w.ntiles;
   const bool kv_mixed = kPacked && key0 + 128 > row1;  // the key block reaches past the end
 
@@ -1465,9 +1559,11 @@ __global__ void __launch_bounds__(kSeqHThreads + (kPacked ? 32 : 0), 1)
       };
       // dP before S in every tile: the commit of S then also covers dP, so the P/dS warps
       // wait for S alone
-      wait_qdo(0);
-      issue_dp(0, h);
-      issue_s(0, h);
+      if (!kPacked || ntiles > 0) {
+        wait_qdo(0);
+        issue_dp(0, h);
+        issue_s(0, h);
+      }
       mbar_wait(bar(bars->acc_zero), 0, abort_flag);
       tc_fence_after();
       for (int i = 0; i < ntiles; ++i) {
@@ -1642,7 +1738,7 @@ __global__ void __launch_bounds__(kSeqHThreads + (kPacked ? 32 : 0), 1)
     tc_fence_after();
     const bool kvalid = key < row1;
     const long long koff = ((long long)bg * a.T + (kvalid ? key : 0)) * D;
-    {
+    if (!shared_walk) {
       const uint32_t tsrc = (g ? tDK : tDV) + lane_base;
       __nv_bfloat16* dst = (g ? a.dk : a.dv) + koff;
 #pragma unroll
@@ -1710,6 +1806,13 @@ __global__ void __launch_bounds__(kSeqHThreads + (kPacked ? 32 : 0), 1)
       case 16: dq_readout<16, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
       default: dq_readout<0, kPacked>(a, bars, tmem, lane_base, c, bg, w); break;
     }
+  }
+
+  if (shared_walk) {
+    __syncwarp();
+    join_keys<D>(a, w, warp < 8, (warp >> 2) & 1, int(threadIdx.x & 127),
+                 ((warp >> 2) & 1 ? tDK : tDV) + (uint32_t((warp & 3) * 32) << 16),
+                 reinterpret_cast<float4*>(smem + Cfg::kOffQ));
   }
 
   tc_fence_before();
@@ -1823,6 +1926,15 @@ inline BwdLayout bwd_layout(const Problem& p) {
       p.d == 128 ? size_t(p.B) * p.Hkv * tile_geom(p).nqt * kRowTermBytes : 0;
   l.acc = l.rt + rt_bytes;
   return l;
+}
+
+// CTAs that share the walk of one key block of a packed batch.
+constexpr int kWalkTwo = 6 * 148, kWalkFour = 74;
+int walk_ctas(const Problem& p) {
+  // key blocks, about: each sequence ends in a block that is half full
+  const long long blocks =
+      (long long)p.B * p.Hkv * (p.T / 128 + (p.nseq < p.T ? p.nseq : p.T) / 2);
+  return blocks <= kWalkFour ? 4 : (blocks <= kWalkTwo ? 2 : 1);
 }
 
 template <int D>
@@ -1950,24 +2062,47 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
     sa.scale_log2 = p.scale * kLog2eBwd;
     sa.cu = p.cu;
     sa.nseq = p.nseq;
+    sa.cl = p.cu ? walk_ctas(p) : 1;
+    // the packed kernels' launch: clusters of sa.cl CTAs
+    auto launch_packed = [&](auto kernel, int threads, int smem, unsigned jobs, auto... args) {
+      cudaError_t err =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err != cudaSuccess) return err;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(jobs * sa.cl);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = stream;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = sa.cl;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      return cudaLaunchKernelEx(&cfg, kernel, args...);
+    };
     const unsigned nkb =
         unsigned(p.cu ? packed_pieces_bound(p.T, p.nseq, 128) : (p.T + 127) / 128);
     if constexpr (D == 128) {
-      auto run = [&](auto kernel, int threads) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (p.cu) {
+        e = launch_packed(moda_bwd_seq_h_kernel<true>, kSeqHThreads + 32, SeqCfg<128>::kSmemBytes,
+                          unsigned(BG) * nkb, mQ, mDO, mK, mV, sa);
+        if (e != cudaSuccess) {
+          *why = "sequence backward launch (halves) failed";
+          return e;
+        }
+      } else {
+        e = cudaFuncSetAttribute(moda_bwd_seq_h_kernel<false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SeqCfg<128>::kSmemBytes);
         if (e != cudaSuccess) {
           *why = "cudaFuncSetAttribute(sequence backward, halves) failed";
-          return;
+          return e;
         }
-        kernel<<<unsigned(BG) * nkb, threads, SeqCfg<128>::kSmemBytes, stream>>>(mQ, mDO, mK, mV,
-                                                                                 sa);
-      };
-      if (p.cu)
-        run(moda_bwd_seq_h_kernel<true>, kSeqHThreads + 32);
-      else
-        run(moda_bwd_seq_h_kernel<false>, kSeqHThreads);
-      if (e != cudaSuccess) return e;
+        moda_bwd_seq_h_kernel<false><<<unsigned(BG) * nkb, kSeqHThreads, SeqCfg<128>::kSmemBytes,
+                                       stream>>>(mQ, mDO, mK, mV, sa);
+      }
     } else {
       CUtensorMap mDQ;
       // fp32 dq accumulator viewed like q: [bg][t][head-in-group][c]; a box is 32 columns
@@ -1984,19 +2119,24 @@ cudaError_t launch_backward_d(const Problem& p, const void* q, const void* k, co
         *why = "cuTensorMapEncodeTiled failed for the dq accumulator";
         return cudaErrorInvalidValue;
       }
-      auto run = [&](auto kernel, int threads, int smem) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (p.cu) {
+        e = launch_packed(moda_bwd_seq_kernel<D, true>, kSeqPackedThreads, SeqCfg<D>::kSmemPacked,
+                          unsigned(BG) * nkb, mQ, mDO, mK, mV, mDQ, sa);
+        if (e != cudaSuccess) {
+          *why = "sequence backward launch failed";
+          return e;
+        }
+      } else {
+        e = cudaFuncSetAttribute(moda_bwd_seq_kernel<D, false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SeqCfg<D>::kSmemBytes);
         if (e != cudaSuccess) {
           *why = "cudaFuncSetAttribute(sequence backward) failed";
-          return;
+          return e;
         }
-        kernel<<<unsigned(BG) * nkb, threads, smem, stream>>>(mQ, mDO, mK, mV, mDQ, sa);
-      };
-      if (p.cu)
-        run(moda_bwd_seq_kernel<D, true>, kSeqPackedThreads, SeqCfg<D>::kSmemPacked);
-      else
-        run(moda_bwd_seq_kernel<D, false>, kSeqThreads, SeqCfg<D>::kSmemBytes);
-      if (e != cudaSuccess) return e;
+        moda_bwd_seq_kernel<D, false><<<unsigned(BG) * nkb, kSeqThreads, SeqCfg<D>::kSmemBytes,
+                                        stream>>>(mQ, mDO, mK, mV, mDQ, sa);
+      }
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) {

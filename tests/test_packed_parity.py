@@ -46,6 +46,11 @@ CASES = [
     ("big-g64-d64", [100, 3, 200], 1, 1, 64, 1, 64, 5, True),
     ("big-full-g4", [700, 129, 1500, 1], 4, 3, 8, 2, 128, 5, False),
     ("big-full-g3", [1500, 90, 1700], 0, 3, 6, 2, 64, 3, False),
+    # enough key blocks for a CTA each in the backward (the ones above share a block's walk)
+    ("big-g1-d64-16-heads", [900, 1100, 1000, 127, 1, 1300, 950, 1029, 700, 800], 0, 3, 16, 16, 64,
+     2, True),
+    ("big-g1-d128-16-heads", [1000, 1200, 800, 129, 0, 1100, 950, 1029, 700, 900], 1, 0, 16, 16,
+     128, 3, True),
     ("big-many", [(13 * i) % 61 for i in range(100)], 2, 2, 16, 4, 128, 4, True),
 ]
 IDS = [c[0] for c in CASES]
