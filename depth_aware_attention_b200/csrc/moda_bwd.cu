@@ -1928,13 +1928,19 @@ inline BwdLayout bwd_layout(const Problem& p) {
   return l;
 }
 
-// CTAs that share the walk of one key block of a packed batch.
-constexpr int kWalkTwo = 6 * 148, kWalkFour = 74;
+// CTAs that share the walk of one key block of a packed batch: as many as fill the GPU while
+// the blocks are few; two also for up to two waves of blocks whose walks are long, which then
+// end more evenly.  Each CTA more costs about as much as two tiles.  (Forward and backward, 16
+// heads in groups of 4, d = 128: 600 tokens, 24 blocks, 82 / 66 / 59 us with 1 / 2 / 4 CTAs; 3000
+// in 20 sequences, 133 blocks, 197 / 158 / 207; 6000 in 10, 207 blocks of about 9 tiles, 367 /
+// 311 / 392; 8000 in 60, 370 blocks of 2 tiles, 316 / 352 / 500.)
 int walk_ctas(const Problem& p) {
-  // key blocks, about: each sequence ends in a block that is half full
-  const long long blocks =
-      (long long)p.B * p.Hkv * (p.T / 128 + (p.nseq < p.T ? p.nseq : p.T) / 2);
-  return blocks <= kWalkFour ? 4 : (blocks <= kWalkTwo ? 2 : 1);
+  const int nseq = p.nseq < p.T ? p.nseq : p.T;
+  // each sequence ends in a block that is half full; a causal walk sees half the sequence
+  const long long blocks = (long long)p.Hkv * (p.T / 128 + nseq / 2);
+  const int tiles = p.T / nseq / (128 / p.G) / 2;
+  if (blocks <= 64) return 4;
+  return blocks <= 148 || (blocks <= 296 && tiles >= 8) ? 2 : 1;
 }
 
 template <int D>
