@@ -525,17 +525,15 @@ def depth_kv_write(x, w, kd, vd, slot):
 
 
 # ---------------------------------------------------------------- ragged batches
-def _checked(device, specs, workspace=None):
-    """_validate for a list of (name, tensor, shape, dtype), written for the calls whose
-    kernels take a few microseconds: one pass of cheap comparisons, and _validate (which
-    says what is wrong) only when one of them fails."""
-    ok = device.type == "cuda" and (workspace is None or (workspace.is_contiguous()
-                                                          and workspace.device == device))
-    for _, t, shape, dtype in specs:
-        ok = (ok and t is not None and t.shape == shape and t.dtype is dtype
-              and t.is_contiguous() and t.device == device)
-    if not ok:
-        _validate(device, {n: (t, shape, dtype) for n, t, shape, dtype in specs}, workspace)
+def _fits(index, shape, dtype, *tensors):
+    """Whether every tensor has this shape and dtype and is contiguous on CUDA device `index`.
+    The kernels of these calls take a few microseconds, and so would _validate: it is run only
+    when this says no, to say what is wrong."""
+    for t in tensors:
+        if (t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != index
+                or not t.is_contiguous()):
+            return False
+    return index >= 0
 
 
 def _call(fn, name, device, *args):
@@ -543,7 +541,7 @@ def _call(fn, name, device, *args):
     current device for the call when it is not.  (torch.cuda.current_stream() builds a Stream
     object, 2 us of a small call's 15; the raw handle takes 0.1.)"""
     import torch
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
@@ -585,13 +583,17 @@ def forward_packed(q, k, v, cu_seqlens, kd=None, vd=None, scale=None, causal=Tru
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((Hq, N), device=q.device, dtype=torch.float32)
-    bf = torch.bfloat16
-    spec = [("q", q, (Hq, N, d), bf), ("k", k, (Hkv, N, d), bf), ("v", v, (Hkv, N, d), bf),
-            ("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32), ("out", out, (Hq, N, d), bf),
-            ("lse", lse, (Hq, N), torch.float32)]
-    if L:
-        spec += [("kd", kd, (Hkv, N, L, d), bf), ("vd", vd, (Hkv, N, L, d), bf)]
-    _checked(q.device, spec)
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.get_device()
+    qs, kv, ds = (Hq, N, d), (Hkv, N, d), (Hkv, N, L, d)
+    if not (_fits(dev, qs, bf, q, out) and _fits(dev, kv, bf, k, v)
+            and _fits(dev, (Hq, N), f32, lse) and _fits(dev, (nseq + 1,), i32, cu_seqlens)
+            and (L == 0 or _fits(dev, ds, bf, kd, vd))):
+        spec = dict(q=(q, qs, bf), k=(k, kv, bf), v=(v, kv, bf),
+                    cu_seqlens=(cu_seqlens, (nseq + 1,), i32), out=(out, qs, bf),
+                    lse=(lse, (Hq, N), f32))
+        if L:
+            spec.update(kd=(kd, ds, bf), vd=(vd, ds, bf))
+        _validate(q.device, spec)
     _call(lib.moda_forward_packed, "moda_forward_packed", q.device, _at(q), _at(k), _at(v),
           _at(kd) if L else None, _at(vd) if L else None, _at(cu_seqlens), _at(out), _at(lse), Hq,
           Hkv, N, nseq, L, d, scale, 1 if causal else 0)
@@ -616,15 +618,21 @@ def backward_packed(q, k, v, cu_seqlens, kd, vd, out, lse, dout, scale=None, cau
             g[name] = None
         elif g.get(name) is None:
             g[name] = torch.empty_like(like)
-    bf, qs, kv, ds = torch.bfloat16, (Hq, N, d), (Hkv, N, d), (Hkv, N, L, d)
-    spec = [("q", q, qs, bf), ("k", k, kv, bf), ("v", v, kv, bf),
-            ("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32), ("out", out, qs, bf),
-            ("lse", lse, (Hq, N), torch.float32), ("dout", dout, qs, bf), ("dq", g["dq"], qs, bf),
-            ("dk", g["dk"], kv, bf), ("dv", g["dv"], kv, bf)]
-    if L:
-        spec += [("kd", kd, ds, bf), ("vd", vd, ds, bf), ("dkd", g["dkd"], ds, bf),
-                 ("dvd", g["dvd"], ds, bf)]
-    _checked(q.device, spec, workspace)
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.get_device()
+    qs, kv, ds = (Hq, N, d), (Hkv, N, d), (Hkv, N, L, d)
+    if not (_fits(dev, qs, bf, q, out, dout, g["dq"])
+            and _fits(dev, kv, bf, k, v, g["dk"], g["dv"]) and _fits(dev, (Hq, N), f32, lse)
+            and _fits(dev, (nseq + 1,), i32, cu_seqlens)
+            and (L == 0 or _fits(dev, ds, bf, kd, vd, g["dkd"], g["dvd"]))
+            and workspace.is_contiguous() and workspace.get_device() == dev):
+        spec = dict(q=(q, qs, bf), k=(k, kv, bf), v=(v, kv, bf),
+                    cu_seqlens=(cu_seqlens, (nseq + 1,), i32), out=(out, qs, bf),
+                    lse=(lse, (Hq, N), f32), dout=(dout, qs, bf), dq=(g["dq"], qs, bf),
+                    dk=(g["dk"], kv, bf), dv=(g["dv"], kv, bf))
+        if L:
+            spec.update(kd=(kd, ds, bf), vd=(vd, ds, bf), dkd=(g["dkd"], ds, bf),
+                        dvd=(g["dvd"], ds, bf))
+        _validate(q.device, spec, workspace)
     _call(lib.moda_backward_packed, "moda_backward_packed", q.device, _at(q), _at(k), _at(v),
           _at(kd) if L else None, _at(vd) if L else None, _at(cu_seqlens), _at(out), _at(lse),
           _at(dout), _at(g["dq"]), _at(g["dk"]), _at(g["dv"]), _at(g["dkd"]), _at(g["dvd"]),
@@ -664,14 +672,18 @@ def tree_decode(q, k, v, kt, vt, parents, lengths, kd=None, vd=None, scale=None,
     if workspace is None:
         workspace = torch.empty(_tree_workspace_size(B, Hq, Hkv, S, N, L, d), device=q.device,
                                 dtype=torch.uint8)
-    bf, new = torch.bfloat16, (B, Hkv, N, d)
-    spec = [("q", q, (B, Hq, N, d), bf), ("k", k, (B, Hkv, S, d), bf), ("v", v, (B, Hkv, S, d), bf),
-            ("kt", kt, new, bf), ("vt", vt, new, bf), ("parents", parents, (B, N), torch.int32),
-            ("lengths", lengths, (B,), torch.int32), ("out", out, (B, Hq, N, d), bf),
-            ("lse", lse, (B, Hq, N), torch.float32)]
-    if L:
-        spec += [("kd", kd, (B, Hkv, N, L, d), bf), ("vd", vd, (B, Hkv, N, L, d), bf)]
-    _checked(q.device, spec, workspace)
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.get_device()
+    qs, kv, new, ds = (B, Hq, N, d), (B, Hkv, S, d), (B, Hkv, N, d), (B, Hkv, N, L, d)
+    if not (_fits(dev, qs, bf, q, out) and _fits(dev, kv, bf, k, v) and _fits(dev, new, bf, kt, vt)
+            and _fits(dev, (B, N), i32, parents) and _fits(dev, (B,), i32, lengths)
+            and _fits(dev, (B, Hq, N), f32, lse) and (L == 0 or _fits(dev, ds, bf, kd, vd))
+            and workspace.is_contiguous() and workspace.get_device() == dev):
+        spec = dict(q=(q, qs, bf), k=(k, kv, bf), v=(v, kv, bf), kt=(kt, new, bf),
+                    vt=(vt, new, bf), parents=(parents, (B, N), i32), lengths=(lengths, (B,), i32),
+                    out=(out, qs, bf), lse=(lse, (B, Hq, N), f32))
+        if L:
+            spec.update(kd=(kd, ds, bf), vd=(vd, ds, bf))
+        _validate(q.device, spec, workspace)
     _call(lib.moda_tree_decode, "moda_tree_decode", q.device, _at(q), _at(k), _at(v), _at(kt),
           _at(vt), _at(kd) if L else None, _at(vd) if L else None, _at(parents), _at(lengths),
           _at(out), _at(lse), _at(workspace), _nbytes(workspace), B, Hq, Hkv, S, N, L, d, scale)
@@ -695,11 +707,13 @@ def cache_score(q, k, lse, lengths, score, scale=None, out=None):
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(score)
-    f32 = torch.float32
-    _checked(q.device, [("q", q, (B, Hq, N, d), torch.bfloat16),
-                        ("k", k, (B, Hkv, S, d), torch.bfloat16), ("lse", lse, (B, Hq, N), f32),
-                        ("lengths", lengths, (B,), torch.int32),
-                        ("score", score, (B, Hkv, S), f32), ("out", out, (B, Hkv, S), f32)])
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, q.get_device()
+    qs, kv, per_key = (B, Hq, N, d), (B, Hkv, S, d), (B, Hkv, S)
+    if not (_fits(dev, qs, bf, q) and _fits(dev, kv, bf, k) and _fits(dev, (B, Hq, N), f32, lse)
+            and _fits(dev, (B,), i32, lengths) and _fits(dev, per_key, f32, score, out)):
+        _validate(q.device, dict(q=(q, qs, bf), k=(k, kv, bf), lse=(lse, (B, Hq, N), f32),
+                                 lengths=(lengths, (B,), i32), score=(score, per_key, f32),
+                                 out=(out, per_key, f32)))
     _call(lib.moda_cache_score, "moda_cache_score", q.device, _at(q), _at(k), _at(lse),
           _at(lengths), _at(score), _at(out), B, Hq, Hkv, S, N, d, scale)
     return out
@@ -725,13 +739,16 @@ def cache_evict(k, v, score, lengths, keep, sinks=0, recent=0, k_out=None, v_out
     r = dict(k_out=new(k_out, (B, Hkv, keep, d), bf), v_out=new(v_out, (B, Hkv, keep, d), bf),
              score_out=new(score_out, (B, Hkv, keep), f32),
              index=new(index, (B, Hkv, keep), i32), lengths_out=new(lengths_out, (B,), i32))
-    _checked(k.device, [("k", k, (B, Hkv, S, d), bf), ("v", v, (B, Hkv, S, d), bf),
-                        ("score", score, (B, Hkv, S), f32), ("lengths", lengths, (B,), i32),
-                        ("k_out", r["k_out"], (B, Hkv, keep, d), bf),
-                        ("v_out", r["v_out"], (B, Hkv, keep, d), bf),
-                        ("score_out", r["score_out"], (B, Hkv, keep), f32),
-                        ("index", r["index"], (B, Hkv, keep), i32),
-                        ("lengths_out", r["lengths_out"], (B,), i32)])
+    dev, kv, rows, kept = k.get_device(), (B, Hkv, S, d), (B, Hkv, keep, d), (B, Hkv, keep)
+    if not (_fits(dev, kv, bf, k, v) and _fits(dev, (B, Hkv, S), f32, score)
+            and _fits(dev, (B,), i32, lengths, r["lengths_out"])
+            and _fits(dev, rows, bf, r["k_out"], r["v_out"])
+            and _fits(dev, kept, f32, r["score_out"]) and _fits(dev, kept, i32, r["index"])):
+        _validate(k.device, dict(
+            k=(k, kv, bf), v=(v, kv, bf), score=(score, (B, Hkv, S), f32),
+            lengths=(lengths, (B,), i32), k_out=(r["k_out"], rows, bf), v_out=(r["v_out"], rows, bf),
+            score_out=(r["score_out"], kept, f32), index=(r["index"], kept, i32),
+            lengths_out=(r["lengths_out"], (B,), i32)))
     _call(lib.moda_cache_evict, "moda_cache_evict", k.device, _at(k), _at(v), _at(score),
           _at(lengths), _at(r["k_out"]), _at(r["v_out"]), _at(r["score_out"]), _at(r["index"]),
           _at(r["lengths_out"]), B, Hkv, S, keep, sinks, recent, d)
