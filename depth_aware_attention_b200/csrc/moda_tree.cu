@@ -64,7 +64,7 @@ struct TreeCfg {
   static constexpr int kOffKV = kQTiles * kTile;
   static constexpr int kOffML = kOffKV + kStages * kTile;  // [2][128] float2
   static constexpr int kOffBar = kOffML + 2 * 128 * 8;
-  static constexpr int kSmemBytes = kOffBar + 384;
+  static constexpr int kSmemBytes = kOffBar + 896;
 };
 
 struct TreeArgs {
@@ -83,6 +83,7 @@ struct TreeArgs {
   // packed prompts (kPrompt): N is the row count of the token axis
   const int* cu;  // [nseq + 1] first rows of the sequences
   int nseq, causal;
+  long long most;  // upper bound of the number of items
 };
 
 __device__ __forceinline__ int tree_length(const TreeArgs& a, int b, bool report = false) {
@@ -178,6 +179,14 @@ struct TreeWalk {
   }
 };
 
+// Packed prompts: a CTA's items, a tile (or pair of tiles) of one sequence and KV head each.
+// Item number c of all, heaviest first (packed_find), goes to the CTAs in turn and back, so
+// that none gets the heavier one of every round; the CTA's warps find them side by side.
+constexpr int kPromptItems = 32;
+struct PromptItem {
+  int row0, len, t0, g;  // len < 0: none
+};
+
 struct TreeBars {
   uint64_t full[10], empty[10], ready[10];  // ring: landed; released; zeroed where needed
   uint64_t q_full, q_empty;
@@ -186,7 +195,8 @@ struct TreeBars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  TreeWalk walk;  // this CTA's first piece
+  TreeWalk walk;                     // this CTA's first piece
+  PromptItem items[kPromptItems];    // prompts: all of them
 };
 
 // This CTA's first piece (all lanes of a warp); left < 0: there is none.
@@ -267,19 +277,12 @@ __device__ __forceinline__ void ancestor_bits(const int* par, int i, uint32_t (&
   if (p != -1) atomicOr(&g_error_word, kErrInternal);
 }
 
-// The one item of a CTA in a packed batch of prompts: a tile (or pair) of its sequence's
-// tokens against the depth entries and the key blocks up to its last token.
-__device__ __forceinline__ TreeWalk prompt_item(const TreeArgs& a, int tokens) {
-  TreeWalk w;
-  const PackedPiece pc = packed_find(a.cu, a.nseq, a.N, tokens, int(blockIdx.x) / a.Hkv);
-  w.left = pc.found ? 0 : -1;  // (the grid is sized by an upper bound)
-  w.b = pc.first;
-  w.it = int(blockIdx.x) % a.Hkv;
-  w.len = pc.len;
-  w.t0 = pc.p * tokens;
-  w.j0 = 0;
-  w.j1 = w.n = a.ND + ((a.causal ? min(pc.len, w.t0 + tokens) : pc.len) + 127) / 128;
-  return w;
+// (all lanes of a warp)
+__device__ __forceinline__ PromptItem prompt_item(const TreeArgs& a, int tokens, int round) {
+  const int at = round & 1 ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x);
+  const int c = round * int(gridDim.x) + at;
+  const PackedPiece pc = packed_find(a.cu, a.nseq, a.N, tokens, c / a.Hkv);
+  return PromptItem{pc.first, pc.found ? pc.len : -1, pc.p * tokens, c % a.Hkv};
 }
 
 // Where an item's data lie.
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto sKV = [&](int s) { return s0 + Cfg::kOffKV + uint32_t(s) * Cfg::kTile; };
   float2* const ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
   TreeBars* bars = reinterpret_cast<TreeBars*>(smem + Cfg::kOffBar);
-  static_assert(sizeof(TreeBars) <= 384, "barrier space");
+  static_assert(sizeof(TreeBars) <= 896, "barrier space");
   volatile int* abort_flag = &bars->abort;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -322,16 +325,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tma_prefetch_desc(maps[lane]);
   }
 
-  // warp 0 finds this CTA's work while others set up the barriers and the tensor memory
-  if (warp == 0) {
-    TreeWalk w;
-    if constexpr (kPrompt) {
-      w = prompt_item(a, a.TQ * Cfg::kQTiles);
-    } else {
-      w = tree_first(a, tree_plan(a));
-      if (blockIdx.x == 0)
-        for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
+  // warp 0 finds this CTA's work (prompts: every warp an item) while others set up the barriers
+  // and the tensor memory
+  if constexpr (kPrompt) {
+    for (int r = warp; r < kPromptItems; r += kTreeThreads / 32) {
+      if ((long long)r * gridDim.x < a.most) {
+        const PromptItem item = prompt_item(a, a.TQ * Cfg::kQTiles, r);
+        if (lane == 0) bars->items[r] = item;
+      } else if (lane == 0) {
+        bars->items[r].len = -1;
+      }
     }
+  } else if (warp == 0) {
+    const TreeWalk w = tree_first(a, tree_plan(a));
+    if (blockIdx.x == 0)
+      for (int b = lane; b < a.B; b += 32) tree_length(a, b, true);
     if (lane == 0) bars->walk = w;
   }
   if (threadIdx.x == 32) {
@@ -363,7 +371,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const TreeWalk walk0 = bars->walk;
+  // prompts: item `k` of this CTA as a piece; `left` counts the items behind it
+  auto load_item = [&](TreeWalk& w, int k) {
+    const PromptItem t = bars->items[k];
+    w.b = t.row0;
+    w.it = t.g;
+    w.len = t.len;
+    w.t0 = t.t0;
+    w.j0 = 0;
+    w.j1 = w.n =
+        a.ND + ((a.causal ? min(t.len, t.t0 + a.TQ * Cfg::kQTiles) : t.len) + 127) / 128;
+  };
+  TreeWalk walk0;
+  int items = 0;  // prompts: this CTA's items
+  if constexpr (kPrompt) {
+    while (items < kPromptItems && bars->items[items].len >= 0) ++items;
+    walk0.left = items - 1;
+    if (items > 0) load_item(walk0, 0);
+  } else {
+    walk0 = bars->walk;
+  }
+  auto next_piece = [&](TreeWalk& w) {
+    if constexpr (kPrompt) {
+      if (w.left <= 0) return false;
+      --w.left;
+      load_item(w, items - 1 - int(w.left));
+      return true;
+    } else {
+      return w.next(a);
+    }
+  };
   if (walk0.left < 0) {  // no work for this CTA
     if (warp == 9) tmem_dealloc(tmem, 512);
     return;
@@ -419,7 +456,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           if (!ok) break;
         }
-        more = w.next(a);
+        more = next_piece(w);
       }
       if (*abort_flag)  // abort path: what was issued still lands; wait for it before exit
         for (int i = e > NS ? e - NS : 0; i < e; ++i)
@@ -428,7 +465,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       TreeWalk w = walk0;
       int pc = 0;  // piece
       bool more = true;
-      for (; more; ++pc, more = w.next(a)) {
+      for (; more; ++pc, more = next_piece(w)) {
         if (pc > 0 && !mbar_wait(bar(bars->q_empty), (pc - 1) & 1, abort_flag)) break;
         const TreeItem item = item_of(w);
         mbar_expect_tx(bar(bars->q_full),
@@ -465,7 +502,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         c.half = 0;
         c.e += wide(c.j) ? 4 : 2;
         if (++c.j == c.w.j1) {
-          c.live = c.w.next(a);
+          c.live = next_piece(c.w);
           c.j = c.w.j0;
           ++c.pc;
         }
@@ -570,7 +607,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (lane == 0) mbar_arrive(bar(bars->empty[s]));
         }
       }
-      more = w.next(a);
+      more = next_piece(w);
     }
     __syncwarp();
   } else {
@@ -875,7 +912,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->o_free));
       u += units;
-      more = w.next(a);
+      more = next_piece(w);
     }
   }
 
@@ -1040,9 +1077,12 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
     *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
     return e;
   }
-  const unsigned grid =
-      kPrompt ? unsigned(p.Hkv * packed_pieces_bound(p.N, a.nseq, tg.TQ * Cfg::kQTiles))
-              : unsigned(kTreeCtas);
+  // prompts: one CTA per SM takes item after item, up to kPromptItems each
+  unsigned grid = kTreeCtas;
+  if (kPrompt) {
+    const long long each = (a.most + kPromptItems - 1) / kPromptItems;
+    grid = unsigned(a.most < kTreeCtas ? a.most : (each > kTreeCtas ? each : kTreeCtas));
+  }
   moda_tree_kernel<D, kPair, kPrompt><<<grid, kTreeThreads, Cfg::kSmemBytes, stream>>>(
       mQ, mK, mV, mKT, mVT, mKD, mVD, a);
   e = cudaGetLastError();
@@ -1117,25 +1157,37 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
   return t.pair ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
 }
 
-// The forward kernel's pairs of tiles make better use of the tensor cores, single tiles (whose
-// two warpgroups take alternate key blocks) are done sooner.  So single tiles are taken while
-// their CTAs fit the GPU at once, smaller ones as long as that still holds: with few tokens a
-// tile, a depth step holds more of each token's entries.  (16 heads in groups of 4, d = 128,
-// L = 24: 411 tokens 13.1 us against the forward kernel's 21.3; 2000 tokens 42 against 40.)
-// Groups without a dense depth path in the forward kernel run here at any size, in pairs once
-// the pairs fill the GPU (groups of 3, d = 64, L = 7: 5000 tokens, 120 pairs, 27 us in single
-// tiles and 31 in pairs; 9000 tokens, 210 pairs, 50 and 41).
+// The forward kernel's pairs of tiles make better use of the tensor cores; single tiles (whose
+// two warpgroups take alternate key blocks) are done sooner, and here a CTA goes on to its next
+// tile with the loads already under way.  So single tiles are taken
+//   - while their CTAs fit the GPU at once, smaller ones as long as that still holds: with few
+//     tokens a tile, a depth step holds more of each token's entries (16 heads in groups of 4,
+//     d = 128, L = 24: 411 tokens in 5 sequences 13 us against the forward kernel's 21);
+//   - for short sequences, about as long as a tile or shorter, in tiles of up to twice their
+//     length (1500 tokens in 181: 62 us against 103; 4000 in 200: 99 against 134; 4000 in 64, mean
+//     62: 84 against 77, so not there);
+//   - for sequences of up to five tiles when each CTA gets several (12000 tokens in 200, d = 64,
+//     L = 8: 93 us against 124; 16000 in 50, L = 0, mean 320: 145 against 134, so not there).
+// Groups without a dense depth path in the forward kernel run here at any size: in pairs of
+// tiles once single ones no longer fit and sequences are long (groups of 3, d = 64, L = 7: 5000
+// tokens in 37 sequences 26 us in single tiles and 31 in pairs; 9000 in 30, 50 and 41).
 PromptTile prompt_tile(const Problem& p) {
   const int full = 128 / p.G;
+  const int nseq = p.nseq < p.T ? p.nseq : p.T;
   // pieces of a size, about: each sequence ends in a piece that is half full
-  auto pieces = [&](int tokens) {
-    return p.Hkv * ((long long)p.T / tokens + (p.nseq < p.T ? p.nseq : p.T) / 2);
-  };
+  auto pieces = [&](int tokens) { return p.Hkv * ((long long)p.T / tokens + nseq / 2); };
+  const int mean = p.T / nseq;
   const bool dense = p.L == 0 || dense_depth_supported(p);
-  if (pieces(dense ? full : 2 * full) > kTreeCtas)
-    return dense ? PromptTile{0, false} : PromptTile{full, true};
   int tokens = full;
-  while (tokens > 1 && pieces(tokens / 2) <= kTreeCtas) tokens /= 2;
+  if (pieces(dense ? full : 2 * full) <= kTreeCtas) {
+    while (tokens > 1 && pieces(tokens / 2) <= kTreeCtas) tokens /= 2;
+    return PromptTile{tokens, false};
+  }
+  const bool single = dense ? 4 * mean <= 5 * full ||
+                                  (mean <= 5 * full && pieces(full) >= 6 * kTreeCtas)
+                            : mean <= 4 * full;
+  if (!single) return dense ? PromptTile{0, false} : PromptTile{full, true};
+  while (tokens > 8 && tokens / 2 >= 2 * mean) tokens /= 2;
   return PromptTile{tokens, false};
 }
 
@@ -1154,6 +1206,7 @@ cudaError_t launch_prompt(const Problem& p, const PromptTile& tile, const void* 
   a.cu = p.cu;
   a.nseq = p.nseq;
   a.causal = p.causal;
+  a.most = p.Hkv * packed_pieces_bound(p.T, p.nseq, t.TQ * (t.pair ? 2 : 1));
   auto go = [&](auto d_c, auto pair_c) {
     return launch_tree_d<decltype(d_c)::value, decltype(pair_c)::value, true>(
         tp, t, a, q, k, v, nullptr, nullptr, kd, vd, encode, stream, why);
