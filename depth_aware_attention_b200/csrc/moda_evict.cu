@@ -277,9 +277,10 @@ cudaError_t launch_select(const EvictArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // (the limit of every call, not this one's size: calls may come from several threads)
   cudaError_t e = cudaFuncSetAttribute(moda_evict_select_kernel<kCl, kHeld>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(cfg.dynamicSmemBytes));
+                                       kHeld ? kEvictHeld * 4 : 0);
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, moda_evict_select_kernel<kCl, kHeld>, a);
 }

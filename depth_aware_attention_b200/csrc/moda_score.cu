@@ -142,16 +142,17 @@ __device__ __forceinline__ ScoreWalk score_first(const ScoreArgs& a, long long s
 // waited for and stored after them, so that it costs no time of its own), the rest at the end.
 struct TailCopy {
   static constexpr int kEach = 8;  // scores per thread of a unit
-  int u, units, per, at;
+  long long u, units;
+  int per, at;
   __device__ __forceinline__ TailCopy(const ScoreArgs& a, int wg, int thread) {
     per = (a.S + 1023) / 1024;
-    units = a.copy_tail ? a.B * a.Hkv * per : 0;
-    u = 2 * blockIdx.x + wg;
+    units = a.copy_tail ? (long long)a.B * a.Hkv * per : 0;
+    u = 2ll * blockIdx.x + wg;
     at = thread;
   }
   template <typename F>
   __device__ __forceinline__ void each(const ScoreArgs& a, F f) const {
-    const int bg = u / per, c = u - bg * per;
+    const int bg = int(u / per), c = int(u - (long long)bg * per);
     const int lo = score_length(a, bg / a.Hkv);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
