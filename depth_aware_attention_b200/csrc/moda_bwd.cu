@@ -1936,11 +1936,12 @@ inline BwdLayout bwd_layout(const Problem& p) {
 // 311 / 392; 8000 in 60, 370 blocks of 2 tiles, 316 / 352 / 500.)
 int walk_ctas(const Problem& p) {
   const int nseq = p.nseq < p.T ? p.nseq : p.T;
-  // each sequence ends in a block that is half full; a causal walk sees half the sequence
+  // each sequence ends in a block that is half full
   const long long blocks = (long long)p.Hkv * (p.T / 128 + nseq / 2);
-  const int tiles = p.T / nseq / (128 / p.G) / 2;
-  if (blocks <= 64) return 4;
-  return blocks <= 148 || (blocks <= 296 && tiles >= 8) ? 2 : 1;
+  const int tiles = 2 * (p.T / nseq) / (128 / p.G);  // of a longer sequence's first block
+  if (tiles < 2) return 1;
+  if (blocks <= 64 && tiles >= 4) return 4;
+  return blocks <= 148 || (blocks <= 296 && tiles >= 32) ? 2 : 1;
 }
 
 template <int D>

@@ -114,11 +114,15 @@ constexpr int kTreeSwitch = 3;
 struct TreePlan {
   long long total, share;
   int parts;
+  int n0;  // steps of an item of sequence `lane`, the first 32 sequences
   // CTAs of each item of a sequence with n steps per item, and the steps of each of them
-  __device__ __forceinline__ int ctas(int n) const { return int((n + share - 1) / share); }
+  // (parts: the share then fits 32 bits, whose division is much the quicker one)
+  __device__ __forceinline__ int ctas(int n) const {
+    return int((unsigned(n) + unsigned(share) - 1u) / unsigned(share));
+  }
   __device__ __forceinline__ int each(int n) const {
-    const int c = ctas(n);
-    return (n + c - 1) / c;
+    const unsigned c = ctas(n);
+    return int((unsigned(n) + c - 1u) / c);
   }
 };
 
@@ -126,24 +130,30 @@ struct TreePlan {
 __device__ __forceinline__ TreePlan tree_plan(const TreeArgs& a) {
   const int lane = threadIdx.x & 31;
   TreePlan p;
-  long long sum = 0;
-  int most = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    const int n = tree_steps(a, b);
-    sum += n;
-    most = max(most, n);
+  p.n0 = lane < a.B ? tree_steps(a, lane) : 0;
+  int most = p.n0;
+  if (a.B <= 32) {
+    p.total = (long long)__reduce_add_sync(0xffffffffu, p.n0) * a.nit;
+  } else {
+    long long sum = p.n0;
+    for (int b = lane + 32; b < a.B; b += 32) {
+      const int n = tree_steps(a, b);
+      sum += n;
+      most = max(most, n);
+    }
+    p.total = warp_sum(sum) * a.nit;
   }
-  p.total = warp_sum(sum) * a.nit;
   p.share = (p.total + kTreeCtas - 1) / kTreeCtas;
   if (p.share < kTreeMinShare) p.share = kTreeMinShare;
   p.parts = 0;
   if ((long long)a.B * a.nit <= kTreeCtas) {
     most = __reduce_max_sync(0xffffffffu, most);
-    // (a share of p.share + kTreeSwitch or more is not taken, so the search may end there)
+    // (a share of more than p.share + kTreeSwitch is not taken, so the search may end there)
     const int limit = min(int(p.share) + kTreeSwitch, most);
     for (int share = int(p.share); share <= limit; ++share) {
-      int c = 0;
-      for (int b = lane; b < a.B; b += 32) c += (tree_steps(a, b) + share - 1) / share;
+      int c = int((unsigned(p.n0) + unsigned(share) - 1u) / unsigned(share));
+      for (int b = lane + 32; b < a.B; b += 32)
+        c += int((unsigned(tree_steps(a, b)) + unsigned(share) - 1u) / unsigned(share));
       if (__reduce_add_sync(0xffffffffu, c) * a.nit <= kTreeCtas) {
         p.share = share;
         p.parts = 1;
@@ -212,7 +222,7 @@ __device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, const TreePlan
   w.j0 = 0;
   w.t0 = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int steps = b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0;
+    const int steps = b0 == 0 ? p.n0 : (b0 + lane < a.B ? tree_steps(a, b0 + lane) : 0);
     const int mine = p.parts ? p.ctas(steps) : steps;
     int incl = mine;
 #pragma unroll
@@ -228,7 +238,7 @@ __device__ __forceinline__ TreeWalk tree_first(const TreeArgs& a, const TreePlan
       const int at = __shfl_sync(0xffffffffu, incl, src) - n;
       const long long off = s - (before + at) * a.nit;
       w.b = b0 + src;
-      w.it = int(off / n);
+      w.it = off >> 32 ? int(off / n) : int(unsigned(off) / unsigned(n));
       w.j0 = int(off - (long long)w.it * n);
       if (p.parts) {
         const int all = __shfl_sync(0xffffffffu, steps, src), each = p.each(all);
@@ -940,7 +950,7 @@ __global__ void __launch_bounds__(256) moda_tree_join_kernel(const TreeArgs a, i
   const int tile = i / a.TQ, item = g * a.nt + tile / qtiles;
   long long before = 0;
   for (int x = lane; x < b; x += 32) {
-    const int m = tree_steps(a, x);
+    const int m = x < 32 ? plan.n0 : tree_steps(a, x);
     before += plan.parts ? plan.ctas(m) : m;
   }
   before = warp_sum(before) * a.nit;
