@@ -7,7 +7,10 @@
 // itself, and its own L depth entries, in one joint softmax.  N = 1 is single-token decoding
 // over caches of different lengths.  (The pages describe neither.)
 //
-// What bounds it: each cached K/V byte is needed once and serves the G x N rows of its KV
+// What bounds it (one B200, in a graph): 32 caches of 10K-32K keys, one token each, 226 us, 6.5
+// TB/s of the measured 6.57; 61 drafts over 2 caches of up to 64K, 32 heads, 125 us, 0.77
+// PFLOP/s and 3.3 TB/s; 4 caches of 1000, one token, 14 us, two launches' latency.
+// Each cached K/V byte is needed once and serves the G x N rows of its KV
 // head, so up to 128 rows the work is a stream from HBM and the tensor cores have the FLOPs
 // to spare; from 128 to 256 rows both take about as long.
 //
@@ -25,6 +28,10 @@
 //   are read on the device, so a captured graph follows them.  An item inside one CTA is
 //   written directly; the pieces of a cut item go to the workspace as (maximum, sum, fp32
 //   accumulator) and a second launch joins them, in the order of the steps.
+//   Prompts (template flag kPrompt).  The same machinery computes the packed forward of small
+//   batches and of groups the forward kernel has no dense depth path for: an item is a tile (or
+//   pair) of one sequence's tokens, its steps are the depth entries and the key blocks up to its
+//   last token, and a CTA takes up to kPromptItems items one after the other.
 //   Rows that must not be read as values (behind a cache's length, unused slots, tile rows no
 //   entry fills) are zeroed in shared memory by warp 10 before the tensor cores see them: a
 //   weight of zero times an infinity or a NaN is a NaN.
