@@ -62,13 +62,17 @@ constexpr float kLog2eTree = 1.4426950408889634f;
 constexpr float kLn2Tree = 0.6931471805599453f;
 constexpr float kTreeRescale = 8.0f;  // log2 units: O is rescaled only past 256x
 
-template <int D, bool kPair>
+// kThin: 0, or the rows (4 or 16) of the few-row form.
+template <int D, bool kPair, int kThin>
 struct TreeCfg {
   static constexpr int kRegions = D / 64;
   static constexpr int kTile = kRegions * kTreeRegion;
   static constexpr int kQTiles = kPair ? 2 : 1;
   static constexpr int kStages = D == 128 ? (kPair ? 5 : 6) : 10;
-  static constexpr int kOffKV = kQTiles * kTile;
+  // few rows: Q, and P^T of each warpgroup, are 16 rows of 128 bytes a region
+  static constexpr int kQRegion = kThin ? 16 * 128 : kTreeRegion;
+  static constexpr int kOffP = kRegions * kQRegion;
+  static constexpr int kOffKV = kThin ? 3 * kOffP : kQTiles * kTile;
   static constexpr int kOffML = kOffKV + kStages * kTile;  // [2][128] float2
   static constexpr int kOffBar = kOffML + 2 * 128 * 8;
   static constexpr int kSmemBytes = kOffBar + 896;
@@ -309,7 +313,193 @@ struct TreeItem {
   int t0, ntok;  // first token of the item among its sequence's ntok
 };
 
-template <int D, bool kPair, bool kPrompt>
+// OR of a predicate over the n threads of a named barrier.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(uint32_t(p))
+      : "memory");
+  return r != 0;
+}
+
+// The softmax warpgroups of the few-row form (N tokens x G heads <= kRows rows, one tile).  A
+// thread is a key of the block: its lane of S^T holds that key's score of every row, so the
+// exponentials are kRows a thread instead of 128 for each of a few rows, and the products are
+// an eighth of the full tile's.  Each row keeps a reference m that all threads of the warpgroup
+// share; it moves only when a score exceeds it by 2^kTreeRescale, which one barrier with an OR
+// finds out, and l is summed per thread until the piece's end.
+//   scratch: [2 warpgroups][4 warps][16] partial results, [2][16] (m, l), [2][16] ancestor bits
+template <int D, int kRows>
+__device__ __forceinline__ void thin_softmax(const TreeArgs& a, TreeBars* bars,
+                                             const TreeWalk& walk0, uint32_t tmem, uint32_t sp,
+                                             float* scratch) {
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wg = warp >> 2, key = threadIdx.x & 127;  // key of the block; head dimension of O^T
+  const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + lane_base + wg * 32, tO = tmem + lane_base + 64 + wg * 32;
+  float* const red = scratch + wg * 64;                                // [4][16]
+  float2* const ml = reinterpret_cast<float2*>(scratch + 128);        // [2][16]
+  uint32_t* const anc = reinterpret_cast<uint32_t*>(scratch + 192) + wg * 16;
+  const int rows = a.N * a.G;
+  const uint32_t all = (1u << rows) - 1u;  // (rows <= 16)
+  const uint32_t group = (1u << a.G) - 1u;
+  // this key's place in P^T: row r is 128 bytes further, its 16-byte chunk swizzled by r % 8
+  const uint32_t pcol = sp + uint32_t(key >> 6) * (16 * 128) + uint32_t(key & 7) * 2;
+  const uint32_t chunk = uint32_t(key & 63) >> 3;
+  TreeWalk w = walk0;
+  int u = 0, pc = 0;
+  bool more = true;
+  for (; more; ++pc) {
+    const int g = w.it;  // (one tile per KV head)
+    const int* par = a.parents + (long long)w.b * a.N;
+    float m[kRows], l[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+    bool has_o = false;
+    for (int j = w.j0; j < w.j1; ++j) {
+      if (((u + j - w.j0) & 1) != wg) continue;
+      const int unit = u + j - w.j0;
+      uint32_t see;  // rows that see this key
+      if (j < a.ND) {
+        const int tok = key / a.JC, e = j * a.JC + key - tok * a.JC;
+        see = tok < a.N && e < a.L ? group << (tok * a.G) : 0u;
+      } else if (j == a.ND) {
+        if (key < a.N) {
+          uint32_t vis[4];
+          ancestor_bits(par, key, vis);
+          anc[key] = vis[0];
+        }
+        named_bar_sync(2 + wg, 128);
+        see = 0u;
+        if (key < a.N)
+          for (int t = 0; t < a.N; ++t)
+            if ((anc[t] >> key) & 1u) see |= group << (t * a.G);
+      } else {
+        see = (j - a.ND - 1) * 128 + key < w.len ? 0xffffffffu : 0u;
+      }
+      see &= all;
+      mbar_wait(bar(bars->s_full[wg]), (unit >> 1) & 1, abort_flag);
+      tc_fence_after();
+      uint32_t sv[16];
+      tmem_ld16(tS, sv);
+      tmem_wait_ld();
+      float x[kRows];
+      bool over = false;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        x[r] = (see >> r) & 1u ? __uint_as_float(sv[r]) * a.scale_log2 : -INFINITY;
+        over = over || x[r] > m[r] + kTreeRescale;
+      }
+      if (named_bar_or(2 + wg, 128, over)) {
+        // new references: the block's maxima
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          float v = x[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          if (lane == 0) red[(warp & 3) * 16 + r] = v;
+        }
+        named_bar_sync(2 + wg, 128);
+        float f[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) f[r] = 1.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float n = fmaxf(fmaxf(fmaxf(red[r], red[16 + r]), fmaxf(red[32 + r], red[48 + r])),
+                                m[r]);
+          f[r] = ex2(m[r] - (n == -INFINITY ? 0.f : n));
+          m[r] = n;
+          l[r] *= f[r];
+        }
+        if (has_o) {  // every product of this warpgroup so far has finished (see the full form)
+          uint32_t o[16];
+          tmem_ld16(tO, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+          tmem_st16(tO, o);
+          tmem_wait_st();
+        }
+      }
+      has_o = true;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float p = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+        l[r] += p;
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pcol + r * 128 + ((chunk ^ (r & 7)) << 4)),
+                     "h"(bf16_bits(p))
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars->p_full[wg]));
+    }
+    // ---- the piece's end: sums over the keys, both warpgroups' states merged
+    const int units = w.j1 - w.j0;
+    named_bar_sync(2 + wg, 128);  // (red's last readers)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+      if (lane == 0) red[(warp & 3) * 16 + r] = l[r];
+    }
+    named_bar_sync(2 + wg, 128);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (key == r)
+        ml[wg * 16 + r] = make_float2(m[r], red[r] + red[16 + r] + red[32 + r] + red[48 + r]);
+    mbar_wait(bar(bars->o_final), pc & 1, abort_flag);
+    tc_fence_after();
+    named_bar_sync(1, 256);
+    const bool whole = w.j0 == 0 && w.j1 == w.n;
+    const bool use0 = units > 1 || (u & 1) == 0, use1 = units > 1 || (u & 1) == 1;
+    uint32_t o0[16], o1[16];
+    tmem_ld16(tmem + lane_base + 64, o0);
+    tmem_ld16(tmem + lane_base + 96, o1);
+    tmem_wait_ld();
+    const int slot = 2 * int(blockIdx.x) + (pc > 0 ? 1 : 0);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if ((r & 1) != wg || r >= rows) continue;
+      const float2 x = ml[r], y = ml[16 + r];
+      const float M = fmaxf(x.x, y.x), mu = M == -INFINITY ? 0.f : M;
+      const float f0 = ex2(x.x - mu), f1 = ex2(y.x - mu);
+      const float L = x.y * f0 + y.y * f1;
+      const float v = (use0 ? f0 * __uint_as_float(o0[r]) : 0.f) +
+                      (use1 ? f1 * __uint_as_float(o1[r]) : 0.f);
+      const int tok = r / a.G, hl = r - tok * a.G;
+      if (whole) {
+        const long long row = ((long long)w.b * a.Hq + g * a.G + hl) * a.N + tok;
+        const bool none = L == 0.f || __ldg(par + tok) == -2;
+        a.out[row * D + key] = __float2bfloat16_rn(none ? 0.f : v / L);
+        if (key == 0) a.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2Tree;
+      } else {
+        const long long wrow = (long long)slot * a.rows + r;
+        a.ws_acc[wrow * D + key] = v;
+        if (key == 0) *reinterpret_cast<float2*>(a.ws_ml + wrow * 2) = make_float2(M, L);
+      }
+    }
+    named_bar_sync(1, 256);  // (the next piece writes the scratch again)
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bars->o_free));
+    u += units;
+    more = w.next(a);
+  }
+}
+
+template <int D, bool kPair, bool kPrompt, int kThin>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     moda_tree_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
@@ -318,7 +508,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                      const __grid_constant__ CUtensorMap tmVT,
                      const __grid_constant__ CUtensorMap tmKD,
                      const __grid_constant__ CUtensorMap tmVD, const TreeArgs a) {
-  using Cfg = TreeCfg<D, kPair>;
+  using Cfg = TreeCfg<D, kPair, kThin>;
+  static_assert(!kThin || (D == 128 && !kPair && !kPrompt), "the few-row form");
   constexpr int NS = Cfg::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the joining grid may be scheduled now: it waits for this grid's completion itself
@@ -330,6 +521,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
   const uint32_t s0 = smem_u32(smem);
   auto sQ = [&](int t) { return s0 + uint32_t(t) * Cfg::kTile; };
+  auto sP = [&](int wg) { return s0 + uint32_t(wg + 1) * Cfg::kOffP; };  // (few rows)
   auto sKV = [&](int s) { return s0 + Cfg::kOffKV + uint32_t(s) * Cfg::kTile; };
   float2* const ml = reinterpret_cast<float2*>(smem + Cfg::kOffML);
   TreeBars* bars = reinterpret_cast<TreeBars*>(smem + Cfg::kOffBar);
@@ -489,7 +681,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                        uint32_t(Cfg::kQTiles * Cfg::kRegions) * 128u * a.G * a.TQ);
         for (int t = 0; t < Cfg::kQTiles; ++t)
           for (int rg = 0; rg < Cfg::kRegions; ++rg)
-            tma_load_4d(sQ(t) + rg * kTreeRegion, &tmQ, bar(bars->q_full), rg * 64, 0,
+            tma_load_4d(sQ(t) + rg * Cfg::kQRegion, &tmQ, bar(bars->q_full), rg * 64, 0,
                         item.tok + t * a.TQ, item.bg);
       }
       if (*abort_flag && pc > 0) mbar_wait_drain(bar(bars->q_full), (pc - 1) & 1);
@@ -501,8 +693,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // S(0) S(1) { PV(u) S(u+2) }: while one warpgroup turns its S into P the tensor cores
     // work for the other.  S(u+2) overwrites P(u), which PV(u), issued before it, has read.
     if (elect_one()) {
-      constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t idesc_o = make_idesc_bf16(128, D, 0, 1);
+      // few rows: S^T = K Q^T (keys x rows), O^T = V^T P^T (d x rows; V is MN-major)
+      constexpr uint32_t idesc_s = make_idesc_bf16(128, kThin ? 16 : 128, 0, 0);
+      constexpr uint32_t idesc_o =
+          kThin ? make_idesc_bf16(128, 16, 1, 0) : make_idesc_bf16(128, D, 0, 1);
       struct Cursor {
         TreeWalk w;
         int j, half, e, pc, u;  // step, tile of the pair, ring entry, piece, unit
@@ -534,7 +728,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (ks / 4) * kTreeRegion + (ks % 4) * 32;
-          mma_ss(tmem + wg * 128, make_sdesc_sw128(sQ(kPair ? c.half : 0) + off, 16, 1024),
+          if constexpr (kThin)
+            mma_ss(tmem + wg * 32, make_sdesc_sw128(sKV(e % NS) + off, 16, 1024),
+                   make_sdesc_sw128(sQ(0) + (ks / 4) * Cfg::kQRegion + (ks % 4) * 32, 16, 1024),
+                   idesc_s, ks > 0 ? 1u : 0u);
+          else
+            mma_ss(tmem + wg * 128, make_sdesc_sw128(sQ(kPair ? c.half : 0) + off, 16, 1024),
                  make_sdesc_sw128(sKV(e % NS) + off, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
         }
         tc_commit(bar(bars->s_full[wg]));
@@ -552,6 +751,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           mbar_wait(bar(bars->o_free), (c.pc - 1) & 1, abort_flag);
         // this warpgroup's first product of the piece overwrites its accumulator
         const bool fresh = kPair ? c.j == c.w.j0 : c.j - c.w.j0 < 2;
+        if constexpr (kThin) {
+          mbar_wait(bar(bars->p_full[wg]), (c.u >> 1) & 1, abort_flag);
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss(tmem + 64 + wg * 32,
+                   make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024),
+                   make_sdesc_sw128(sP(wg) + (ks / 4) * Cfg::kQRegion + (ks % 4) * 32, 16, 1024),
+                   idesc_o, (ks > 0 || !fresh) ? 1u : 0u);
+        } else {
         // keys [0, 64) as soon as their P is in, then the rest
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -564,6 +773,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
                    (ks > 0 || !fresh) ? 1u : 0u);
           }
+        }
         }
         if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
         if (c.j == c.w.j1 - 1 && (!kPair || c.half == 1)) tc_commit(bar(bars->o_final));
@@ -627,6 +837,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       more = next_piece(w);
     }
     __syncwarp();
+  } else if constexpr (kThin != 0) {
+    thin_softmax<D, kThin>(a, bars, walk0, tmem, sP(warp >> 2),
+                           reinterpret_cast<float*>(smem + Cfg::kOffML));
   } else {
     // ------------------------------------------------------------ softmax warpgroups
     const int wg = warp >> 2;
@@ -1037,12 +1250,12 @@ TreeGeom tree_geom(int N, int G, int L) {
   return t;
 }
 
-template <int D, bool kPair, bool kPrompt>
+template <int D, bool kPair, bool kPrompt, int kThin = 0>
 cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeArgs& a,
                           const void* q, const void* k, const void* v, const void* kt,
                           const void* vt, const void* kd, const void* vd, EncodeTiledFn encode,
                           cudaStream_t stream, const char** why) {
-  using Cfg = TreeCfg<D, kPair>;
+  using Cfg = TreeCfg<D, kPair, kThin>;
   const cuuint64_t E = 2, BG = cuuint64_t(p.B) * p.Hkv;
   auto map = [&](CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                  const cuuint64_t* str, const cuuint32_t* box) {
@@ -1087,7 +1300,7 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
     *why = "cuTensorMapEncodeTiled failed for the tree attention's tensors";
     return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(moda_tree_kernel<D, kPair, kPrompt>,
+  cudaError_t e = cudaFuncSetAttribute(moda_tree_kernel<D, kPair, kPrompt, kThin>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg::kSmemBytes);
   if (e != cudaSuccess) {
@@ -1100,7 +1313,7 @@ cudaError_t launch_tree_d(const TreeProblem& p, const TreeGeom& tg, const TreeAr
     const long long each = (a.most + kPromptItems - 1) / kPromptItems;
     grid = unsigned(a.most < kTreeCtas ? a.most : (each > kTreeCtas ? each : kTreeCtas));
   }
-  moda_tree_kernel<D, kPair, kPrompt><<<grid, kTreeThreads, Cfg::kSmemBytes, stream>>>(
+  moda_tree_kernel<D, kPair, kPrompt, kThin><<<grid, kTreeThreads, Cfg::kSmemBytes, stream>>>(
       mQ, mK, mV, mKT, mVT, mKD, mVD, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) {
@@ -1169,6 +1382,14 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
   };
   using D128 = std::integral_constant<int, 128>;
   using D64 = std::integral_constant<int, 64>;
+  // Few rows: the transposed products.  (d = 64 has no such form: its O^T would have 64 lanes.)
+  const int rows = p.N * (p.Hq / p.Hkv);
+  if (p.d == 128 && rows <= 4)
+    return launch_tree_d<128, false, false, 4>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
+                                               why);
+  if (p.d == 128 && rows <= 16)
+    return launch_tree_d<128, false, false, 16>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
+                                                why);
   if (p.d == 128)
     return t.pair ? go(D128{}, std::true_type{}) : go(D128{}, std::false_type{});
   return t.pair ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});

@@ -37,6 +37,16 @@ CASES = [
     ("g64-one", [140, 0], 140, 1, 64, 1, 64, 3, "line"),
     ("long-L", [50, 0], 64, 6, 4, 1, 128, 130, "random"),
     ("many-sequences", [(37 * i) % 300 for i in range(70)], 300, 2, 4, 1, 64, 2, "line"),
+    # few rows at d = 128: the transposed form, with 4 and with up to 16 rows
+    ("rows-1", [700, 0, 128], 700, 1, 2, 2, 128, 3, "line"),
+    ("rows-2-deep", [129, 4000], 4000, 2, 3, 3, 128, 200, "random"),
+    ("rows-4-tree", [1000, 1, 255], 1024, 4, 2, 2, 128, 5, "random"),
+    ("rows-6-odd", [333, 77], 400, 2, 6, 2, 128, 70, "star"),
+    ("rows-16-tree", [513, 0, 2000], 2000, 8, 4, 2, 128, 9, "random"),
+    ("rows-16-drafts", [1500, 40], 1500, 16, 3, 3, 128, 0, "random"),
+    ("rows-15", [260, 127], 300, 5, 6, 2, 128, 17, "random"),
+    ("rows-16-group", [3000], 3000, 1, 32, 2, 128, 40, "line"),
+    ("rows-many-items", [(53 * i) % 700 for i in range(90)], 700, 1, 8, 4, 128, 24, "line"),
     ("long-64k", [65536, 40000], 65536, 16, 16, 4, 128, 0, "random"),
 ]
 IDS = [c[0] for c in CASES]
