@@ -246,3 +246,23 @@ def test_gradient_against_differences():
         # the directional sum's error: each element off by a few U of its size, independently
         sigma = 4 * (2.0 ** -8) * (grads["d" + n].double() * u).pow(2).sum().sqrt().item()
         assert abs(got - slope) <= 6 * sigma + 1e-3, (n, got, slope)
+
+
+@pytest.mark.parametrize("d,L,G,causal", [(64, 0, 1, True), (128, 0, 1, True), (128, 3, 3, True),
+                                          (64, 5, 4, True), (128, 1, 16, False), (64, 0, 8, False)])
+def test_short_sequences_lose_no_precision(d, L, G, causal):
+    # many sequences of a few tokens: dq's relative error is made of two roundings of the same
+    # size, of dS to bf16 and of dq itself (its row term D comes from the keys), so it is at
+    # most sqrt(2) of the second alone; a tenth more for the fp32 sums and the sample
+    case = ("short", [5, 2, 7, 3, 1, 6] * 40, 0, 0, 2 * G, 2, d, L, causal)
+    x, ends = make(case, 321, dout=True)
+    args = [x[n] for n in ("q", "k", "v", "cu", "kd", "vd")]
+    out, lse = moda.forward_packed(*args, causal=causal)
+    g = moda.backward_packed(*args, out, lse, x["dout"], causal=causal)
+    moda.check_device_errors()
+    off = rounding = 0.0
+    for a, e in zip(ends[:-1], ends[1:]):
+        for _, rows, r in reference(x, a, e, 2 * G, 2, d, causal, dout=True):
+            off += (g["dq"][rows, a:e].double() - r["dq"]).square().sum().item()
+            rounding += (r["dq"].to(BF).double() - r["dq"]).square().sum().item()
+    assert math.sqrt(off) <= 1.1 * math.sqrt(2 * rounding), math.sqrt(off / rounding)
