@@ -105,6 +105,8 @@ struct BwdDepthArgs {
 // this many keys, depth entries included, therefore form D from the keys: sum_j P_j <dO, v_j>.
 // (5 sequences of 25 to 100 tokens: 2.8e-3 from out, 2.5e-3 with 8 keys, 2.4e-3 with 32 or all.
 // With 32 keys one by one the depth kernel of 16K tokens in 24 sequences took 500 us, not 410.)
+// The kernel that looks for such rows is one of its own (kFew), for fewer depth entries than this:
+// among 24 entries no row qualifies, and the code alone cost 391 -> 406 us.
 constexpr int kFewKeys = 16;
 
 // Token rows of a packed batch that belong to a sequence: [lo, hi).
@@ -143,7 +145,8 @@ __host__ __device__ constexpr int bf_head(int lane, int i) {
 
 // kRT: also write the tiled row-term records (a.rt, the d = 128 sequence kernel's input);
 // the instantiation without them is the one depth-only attention and d = 64 run.
-template <int D, int GM, bool kRT, bool kPacked>
+// kFew (packed): rows with at most kFewKeys keys form their row term from the keys.
+template <int D, int GM, bool kRT, bool kPacked, bool kFew>
 // (GM <= 4: at most 168 registers, three CTAs per SM; measured faster than 188 registers
 // and two CTAs)
 __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
@@ -237,15 +240,19 @@ __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
       }
     }
     if constexpr (kPacked) {
-      if (a.L < kFewKeys) {
-        // this token's sequence: the last one that begins at or before it
-        int lo = 0, hi = a.nseq;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(a.cu + mid) <= t)
-            lo = mid;
-          else
-            hi = mid;
+      if constexpr (kFew) {
+        // this token's sequence: the last one that begins at or before it, among the starts that
+        // its slot's lanes read side by side (11 sequences: one step).  lo stays below nseq
+        // whatever the bounds hold.
+        int lo = 0;
+        for (int len = a.nseq; len > 1;) {
+          const int step = (len + NT - 1) / NT;
+          const long long at = lo + (long long)cs * step;
+          const bool before = cs * (long long)step < len && at < a.nseq && __ldg(a.cu + at) <= t;
+          const uint32_t votes = __ballot_sync(0xffffffffu, before);
+          const int n = __popc((votes >> ((tid & 31) / NT * NT)) & ((1u << NT) - 1));
+          lo += max(n - 1, 0) * step;
+          len = step;
         }
         const int first = max(0, __ldg(a.cu + lo)), end = min(a.T, __ldg(a.cu + lo + 1));
         const int n = a.causal ? t - first + 1 : end - first;  // sequence keys it sees
@@ -1980,7 +1987,7 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <int D, int GM, bool kRT, bool kPacked>
+template <int D, int GM, bool kRT, bool kPacked, bool kFew>
 cudaError_t launch_depth_as(const BwdDepthArgs& args, cudaStream_t stream, const char** why) {
   const int tpb = kDepthThreads / (D / 8);
   BwdDepthArgs a = args;
@@ -1992,20 +1999,20 @@ cudaError_t launch_depth_as(const BwdDepthArgs& args, cudaStream_t stream, const
                  : 0;
   // q/dO slots (not needed when they live in registers) + the per-thread cp.async ring
   const size_t smem = (GM <= 4 ? 0 : size_t(tpb) * 2 * a.G * D * 2) + kDepthRingBytes;
-  cudaError_t e = cudaFuncSetAttribute(moda_bwd_depth_kernel<D, GM, kRT, kPacked>,
+  cudaError_t e = cudaFuncSetAttribute(moda_bwd_depth_kernel<D, GM, kRT, kPacked, kFew>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute(depth backward) failed";
     return e;
   }
   int per_sm = 1;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moda_bwd_depth_kernel<D, GM, kRT, kPacked>,
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, moda_bwd_depth_kernel<D, GM, kRT, kPacked, kFew>,
                                                 kDepthThreads, smem);
   if (per_sm < 1) per_sm = 1;
   const long long need = (a.ntok + tpb - 1) / tpb;
   const long long cap = (long long)sm_count() * per_sm;
   const unsigned grid = unsigned(need < cap ? need : cap);
-  moda_bwd_depth_kernel<D, GM, kRT, kPacked><<<grid, kDepthThreads, smem, stream>>>(a);
+  moda_bwd_depth_kernel<D, GM, kRT, kPacked, kFew><<<grid, kDepthThreads, smem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) *why = "depth backward launch failed";
   return e;
@@ -2015,8 +2022,10 @@ template <int D, int GM, bool kRT>
 cudaError_t launch_depth(const BwdDepthArgs& a, cudaStream_t stream, const char** why) {
   // (packed batches always have a sequence part, whose d = 128 kernel reads the records)
   if constexpr (kRT || D == 64)
-    if (a.cu) return launch_depth_as<D, GM, kRT, true>(a, stream, why);
-  return launch_depth_as<D, GM, kRT, false>(a, stream, why);
+    if (a.cu)
+      return a.L < kFewKeys ? launch_depth_as<D, GM, kRT, true, true>(a, stream, why)
+                            : launch_depth_as<D, GM, kRT, true, false>(a, stream, why);
+  return launch_depth_as<D, GM, kRT, false, false>(a, stream, why);
 }
 
 // Byte offsets of the backward's workspace regions: the fp32 dq accumulator [B][Hq][T][d]
