@@ -7,9 +7,9 @@
 // itself, and its own L depth entries, in one joint softmax.  N = 1 is single-token decoding
 // over caches of different lengths.  (The pages describe neither.)
 //
-// What bounds it (one B200, in a graph): 32 caches of 10K-32K keys, one token each, 226 us, 6.5
-// TB/s of the measured 6.57; 61 drafts over 2 caches of up to 64K, 32 heads, 125 us, 0.77
-// PFLOP/s and 3.3 TB/s; 4 caches of 1000, one token, 14 us, two launches' latency.
+// What bounds it (one B200): 32 caches of 10K-32K keys, one token each, 220 us sustained, 6.7
+// TB/s; 61 drafts over 2 caches of up to 64K, 32 heads, 125 us in a graph, 0.77 PFLOP/s and 3.3
+// TB/s; 4 caches of 1000, one token, 11 us in a graph, two launches' latency.
 // Each cached K/V byte is needed once and serves the G x N rows of its KV
 // head, so up to 128 rows the work is a stream from HBM and the tensor cores have the FLOPs
 // to spare; from 128 to 256 rows both take about as long.
@@ -28,6 +28,12 @@
 //   are read on the device, so a captured graph follows them.  An item inside one CTA is
 //   written directly; the pieces of a cut item go to the workspace as (maximum, sum, fp32
 //   accumulator) and a second launch joins them, in the order of the steps.
+//   Few rows (template flag kThin: up to 16 rows, d = 128).  One token of a group of 4 fills 4 of
+//   the 128 rows, and the idle rest costs power and with it the clock, and the softmax's time.
+//   Here the products are transposed, S^T = K Q^T and O^T = V^T P^T, with 16 columns for the
+//   rows: an eighth of the products, and a thread holds one key instead of one row.  (32 caches
+//   of 10K-32K keys, one token: 247 -> 220 us sustained; 4 caches of 1000: 14.0 -> 11.0 in a
+//   graph.)
 //   Prompts (template flag kPrompt).  The same machinery computes the packed forward of small
 //   batches and of groups the forward kernel has no dense depth path for: an item is a tile (or
 //   pair) of one sequence's tokens, its steps are the depth entries and the key blocks up to its
@@ -38,7 +44,8 @@
 //
 // Warp roles (352 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA (lane 0
 // the ring, lane 1 the Q tiles), warp 9 tcgen05 issuer, warp 10 follows the ring and zeroes.
-// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
+// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); few rows: S^T at
+// 0 and 32, O^T at 64 and 96, 16 columns each.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    idesc_s, ks > 0 ? 1u : 0u);
           else
             mma_ss(tmem + wg * 128, make_sdesc_sw128(sQ(kPair ? c.half : 0) + off, 16, 1024),
-                 make_sdesc_sw128(sKV(e % NS) + off, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
+                   make_sdesc_sw128(sKV(e % NS) + off, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
         }
         tc_commit(bar(bars->s_full[wg]));
         if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
@@ -761,19 +768,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    make_sdesc_sw128(sP(wg) + (ks / 4) * Cfg::kQRegion + (ks % 4) * 32, 16, 1024),
                    idesc_o, (ks > 0 || !fresh) ? 1u : 0u);
         } else {
-        // keys [0, 64) as soon as their P is in, then the rest
+          // keys [0, 64) as soon as their P is in, then the rest
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          mbar_wait(bar(half ? bars->p_full[wg] : bars->p_half[wg]), (c.u >> 1) & 1, abort_flag);
-          tc_fence_after();
+          for (int half = 0; half < 2; ++half) {
+            mbar_wait(bar(half ? bars->p_full[wg] : bars->p_half[wg]), (c.u >> 1) & 1,
+                      abort_flag);
+            tc_fence_after();
 #pragma unroll
-          for (int kq = 0; kq < 4; ++kq) {
-            const int ks = half * 4 + kq;
-            mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + ks * 8,
-                   make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
-                   (ks > 0 || !fresh) ? 1u : 0u);
+            for (int kq = 0; kq < 4; ++kq) {
+              const int ks = half * 4 + kq;
+              mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + ks * 8,
+                     make_sdesc_sw128(sKV(e % NS) + ks * 2048, kTreeRegion, 1024), idesc_o,
+                     (ks > 0 || !fresh) ? 1u : 0u);
+            }
           }
-        }
         }
         if (!kPair || two || c.half == 1) tc_commit(bar(bars->empty[e % NS]));
         if (c.j == c.w.j1 - 1 && (!kPair || c.half == 1)) tc_commit(bar(bars->o_final));
