@@ -1390,7 +1390,10 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
   };
   using D128 = std::integral_constant<int, 128>;
   using D64 = std::integral_constant<int, 64>;
-  // Few rows: the transposed products.  (d = 64 has no such form: its O^T would have 64 lanes.)
+  // Few rows: the transposed products, with 4 rows' exponentials a thread or with 16.  (d = 64 has
+  // no such form: its O^T would have 64 lanes.)  In a graph, 4-row form / 16-row form / full tiles:
+  // 4 rows, 4 caches of 1000 keys 12.7 / 15.7 / 15.7 us, 32 of 10K-32K 216 / 221 / 230; 16 rows
+  // (4 tokens), - / 16.1 / 15.7 and - / 228 / 237.
   const int rows = p.N * (p.Hq / p.Hkv);
   if (p.d == 128 && rows <= 4)
     return launch_tree_d<128, false, false, 4>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
