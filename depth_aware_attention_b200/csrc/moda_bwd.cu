@@ -109,10 +109,32 @@ struct BwdDepthArgs {
 // among 24 entries no row qualifies, and the code alone cost 391 -> 406 us.
 constexpr int kFewKeys = 16;
 
-// Token rows of a packed batch that belong to a sequence: [lo, hi).
+// Token rows of a packed batch that belong to a sequence: [lo, hi) where every sequence's bounds
+// are good; lo = -1 where some are not, and packed_owned has to be asked row by row.  (All lanes
+// of a warp.)
 __device__ __forceinline__ void packed_rows(const int* cu, int nseq, int N, int& lo, int& hi) {
-  lo = max(0, __ldg(cu));
-  hi = min(N, __ldg(cu + nseq));
+  bool bad = false;
+  int first;
+  for (int s = threadIdx.x & 31; s < nseq; s += 32) packed_len(cu, s, N, first, bad);
+  bad = __any_sync(0xffffffffu, bad);
+  lo = bad ? -1 : __ldg(cu);
+  hi = __ldg(cu + nseq);
+}
+// Whether row t (of this lane) belongs to a sequence whose bounds are good.  (All lanes of a warp;
+// a step holds 32 sequences.)
+__device__ __forceinline__ bool packed_owned(const int* cu, int nseq, int N, int t) {
+  bool own = false, bad = false;
+  for (int s0 = 0; s0 < nseq && !__all_sync(0xffffffffu, own); s0 += 32) {
+    const int s = s0 + int(threadIdx.x & 31);
+    int first = 0;
+    const int len = s < nseq ? packed_len(cu, s, N, first, bad) : 0;
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      const int a = __shfl_sync(0xffffffffu, first, j), n = __shfl_sync(0xffffffffu, len, j);
+      own = own || (t >= a && t - a < n);
+    }
+  }
+  return own;
 }
 
 // One token slot = D/8 consecutive threads (one 16-byte column chunk each); a CTA works
@@ -190,7 +212,10 @@ __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
     const long long tkc = inside ? tk : a.ntok - 1;
     const long long bg = tkc / a.T;
     const int t = int(tkc - bg * a.T);
-    const bool valid = inside && (!kPacked || (t >= row_lo && t < row_hi));
+    bool valid = inside;
+    if constexpr (kPacked)
+      valid = (row_lo < 0 ? packed_owned(a.cu, a.nseq, a.T, t) : t >= row_lo && t < row_hi) &&
+              inside;
     const int qt = kRT ? t / a.TQ : 0, tq = t - qt * a.TQ;
     float* const rt_tile = kRT ? a.rt + ((bg * a.nqt + qt) << 8) : nullptr;
     const int r0 = tq * a.Gfull + a.head0;  // tile row of this chunk's head 0
@@ -254,10 +279,12 @@ __global__ void __launch_bounds__(kDepthThreads, GM <= 4 ? 3 : 1)
           lo += max(n - 1, 0) * step;
           len = step;
         }
-        const int first = max(0, __ldg(a.cu + lo)), end = min(a.T, __ldg(a.cu + lo + 1));
+        bool bad = false;
+        int first;
+        const int len = packed_len(a.cu, lo, a.T, first, bad), end = first + len;
         const int n = a.causal ? t - first + 1 : end - first;  // sequence keys it sees
-        // (a token of no sequence, where the bounds are out of order: the sum over nothing)
-        const bool few = valid && t >= first && t < end && n + a.L <= kFewKeys;
+        // (where bounds are out of order the sequence found may not be the token's: from out then)
+        const bool few = valid && !bad && t >= first && t < end && n + a.L <= kFewKeys;
         const int keys = few ? n + a.L : 0;
         const int most = __reduce_max_sync(0xffffffffu, keys);
         if (!kReg) __syncwarp();  // q and dO in shared memory, written by the slot's lanes
@@ -1959,10 +1986,13 @@ __global__ void __launch_bounds__(256) moda_dq_convert_packed_kernel(
     const int* __restrict__ cu, int nseq) {
   int lo, hi;
   packed_rows(cu, nseq, N, lo, hi);
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8;
-       i += (long long)gridDim.x * blockDim.x) {
+  const int lane = threadIdx.x & 31;
+  for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x - lane; i0 < n8;
+       i0 += (long long)gridDim.x * blockDim.x) {  // (a warp's lanes stay together)
+    const long long i = i0 + lane;
     const int t = int(unsigned(i >> shift) % unsigned(N));  // (at most 2^31 rows)
-    if (t < lo || t >= hi) continue;
+    const bool own = lo < 0 ? packed_owned(cu, nseq, N, t) : t >= lo && t < hi;
+    if (!own || i >= n8) continue;
     const float4 x = reinterpret_cast<const float4*>(acc)[2 * i];
     const float4 y = reinterpret_cast<const float4*>(acc)[2 * i + 1];
     const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
