@@ -61,6 +61,8 @@ moda_status_t check_packed(const int* cu, int nseq, int Hq, int Hkv, int N, floa
     return fail(MODA_ERR_INVALID_ARGUMENT, "cu_seqlens must be 4-byte aligned");
   if (nseq < 1) return fail(MODA_ERR_INVALID_ARGUMENT, "nseq must be at least 1");
   if (!(scale > 0.f)) return fail(MODA_ERR_INVALID_ARGUMENT, "scale must be positive");
+  if (nseq > (1 << 30))  // (the kernels step through the sequences by 32, in 32 bits)
+    return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");
   const long long unit = 2 * (128 / (Hq / Hkv));  // the smaller piece of the two passes
   if (Hkv * moda::packed_pieces_bound(N, nseq, unit < 128 ? unit : 128) > 0x7fffffffll)
     return fail(MODA_ERR_UNSUPPORTED, "problem too large for the kernels' index ranges");

@@ -37,7 +37,9 @@ __device__ __forceinline__ int packed_len(const int* cu, int s, int N, int& firs
   return e - a;
 }
 
-// Piece number c (all 32 lanes call this together, with the same arguments).
+// Piece number c (all 32 lanes call this together, with the same arguments).  With good bounds every
+// count is below 2^31.  Where entries go back, sequences whose own bounds are good may overlap, and
+// the counts may wrap around: what is found is then some piece of one of them, or none.
 __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int N, int U, int c) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
@@ -46,7 +48,7 @@ __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int 
   // the first 32 sequences' counts stay in a register
   const int n0 = lane < nseq ? pieces(lane) : 0;
   auto total = [&](int p) {
-    int t = max(0, n0 - p);
+    uint32_t t = max(0, n0 - p);
     for (int s = lane + 32; s < nseq; s += 32) t += max(0, pieces(s) - p);
     return __reduce_add_sync(0xffffffffu, t);
   };
@@ -55,16 +57,16 @@ __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int 
   for (int s = lane + 32; s < nseq; s += 32) most = max(most, pieces(s));
   most = __reduce_max_sync(0xffffffffu, most);
   if (__any_sync(0xffffffffu, bad) && threadIdx.x == 0) atomicOr(&g_error_word, kErrInternal);
-  if (c >= total(0)) return r;
+  if (uint32_t(c) >= total(0)) return r;
   int lo = 0, hi = most;  // F(lo) > c >= F(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (total(mid) > c)
+    if (total(mid) > uint32_t(c))
       lo = mid;
     else
       hi = mid;
   }
-  int rank = c - total(lo + 1);
+  int rank = int(uint32_t(c) - total(lo + 1));
   for (int s0 = 0; s0 < nseq; s0 += 32) {
     const int s = s0 + lane;
     const int n = s0 == 0 ? n0 : (s < nseq ? pieces(s) : 0);
@@ -73,7 +75,9 @@ __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int 
     if (rank < here) {
       // the lane that holds the rank-th of these sequences
       const bool mine = n > lo && __popc(m & ((1u << lane) - 1u)) == rank;
-      const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      const uint32_t holder = __ballot_sync(0xffffffffu, mine);
+      if (holder == 0u) return r;  // (a rank below zero, after a wrap)
+      const int src = __ffs(holder) - 1;
       const int len = mine ? packed_len(cu, s, N, first, bad) : 0;
       r.first = __shfl_sync(0xffffffffu, first, src);
       r.len = __shfl_sync(0xffffffffu, len, src);

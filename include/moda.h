@@ -145,9 +145,10 @@ moda_status_t moda_depth_attention_backward(const void *q, const void *kd, const
  * must be finite.
  * The entries must not decrease and must lie in [0, N].  They are known on the device alone:
  * a sequence whose two entries break this is treated as empty and sets bit 2 of the device
- * error word (moda_check_device_errors() returns MODA_ERR_INTERNAL).  The lengths are read
- * when the kernel runs, so a captured graph follows them.
- * nseq >= 1, N >= 1, scale > 0; everything else as moda_forward.  One launch, no workspace.
+ * error word (moda_check_device_errors() returns MODA_ERR_INTERNAL).  Sequences that are left
+ * and overlap, where an entry went back, have undefined results.  The lengths are read when the kernel runs, so a
+ * captured graph follows them.
+ * 1 <= nseq <= 2^30, N >= 1, scale > 0; everything else as moda_forward.  One launch, no workspace.
  */
 moda_status_t moda_forward_packed(const void *q, const void *k, const void *v, const void *kd,
                                   const void *vd, const int32_t *cu_seqlens, void *out,
