@@ -160,7 +160,8 @@ moda_status_t moda_forward_packed(const void *q, const void *k, const void *v, c
  * layouts of moda_forward_packed (whose out and lse it takes).  The gradients' rows outside
  * all sequences are left as they are, and those of the inputs, out, lse and dout are not
  * read into any result.  Bad bounds as there: the other sequences' gradients are what they
- * would be without them.  Rows that see at most 16 keys, depth entries included, take their
+ * would be without them; rows of no sequence that lie between two of those may be overwritten
+ * in dq, dkd and dvd.  Rows that see at most 16 keys, depth entries included, take their
  * row term <dout, out> from the keys instead of from the rounded out.  Workspace:
  * moda_backward_workspace_size(1, Hq, Hkv, N, L, d) bytes.
  * Summation order, launches and everything else as moda_backward.

@@ -1,6 +1,7 @@
 """Packed batches whose bounds break the rules (they are known on the device alone): the sequences
 with the bad entries are treated as empty and reported, and the others are computed as ever, in the
-forward and in the backward.  Rows of no sequence stay as they were."""
+forward and in the backward.  Rows of no sequence stay as they were (in dq, dkd and dvd those before
+the first and behind the last good sequence)."""
 import math
 
 import pytest
@@ -70,5 +71,9 @@ def test_good_sequences_among_bad_bounds(name, unit, G, d, L, causal):
             assert_close(grads["dq"][rows, a:e], r["dq"], r["dq_bound"], what + " dq")
             for n in list(grads)[1:]:
                 assert_close(grads[n][h, a:e], r[n], r[n + "_bound"], f"{what} {n}")
+    between = left.clone()
+    if good:  # (what the backward leaves alone where some bounds are bad)
+        between[good[0][0] * unit:good[-1][1] * unit] = False
     for n, t in dict(grads, out=out, lse=lse).items():
-        assert (t[:, left] == 7.0).all(), f"{name}: {n} was written outside the good sequences"
+        rows = between if n in ("dq", "dkd", "dvd") else left
+        assert (t[:, rows] == 7.0).all(), f"{name}: {n} was written outside the good sequences"
