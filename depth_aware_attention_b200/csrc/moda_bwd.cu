@@ -2070,8 +2070,7 @@ inline BwdLayout bwd_layout(const Problem& p) {
 // 311 / 392; 8000 in 60, 370 blocks of 2 tiles, 316 / 352 / 500.)
 int walk_ctas(const Problem& p) {
   const int nseq = p.nseq < p.T ? p.nseq : p.T;
-  // each sequence ends in a block that is half full
-  const long long blocks = (long long)p.Hkv * (p.T / 128 + nseq / 2);
+  const long long blocks = packed_pieces_estimate(p, 128);
   const int tiles = 2 * (p.T / nseq) / (128 / p.G);  // of a longer sequence's first block
   if (tiles < 2) return 1;
   if (blocks <= 64 && tiles >= 4) return 4;

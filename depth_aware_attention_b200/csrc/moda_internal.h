@@ -38,6 +38,15 @@ inline TileGeom tile_geom(const Problem& p) {
   return t;
 }
 
+// About how many pieces of `unit` tokens a packed batch has over all KV heads, for the choice of a
+// kernel (the lengths are known on the device alone): every sequence ends in a piece that is half
+// full, but a lone one, whose pieces are counted.
+inline long long packed_pieces_estimate(const Problem& p, int unit) {
+  if (p.nseq == 1) return 1LL * p.Hkv * ((p.T + unit - 1) / unit);
+  const long long nseq = p.nseq < p.T ? p.nseq : p.T;
+  return p.Hkv * (2LL * p.T + nseq * unit) / (2 * unit);
+}
+
 // Tensor-map encoder obtained from the driver at run time (no link-time libcuda).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

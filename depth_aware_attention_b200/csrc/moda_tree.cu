@@ -1423,8 +1423,7 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
 PromptTile prompt_tile(const Problem& p) {
   const int full = 128 / p.G;
   const int nseq = p.nseq < p.T ? p.nseq : p.T;
-  // pieces of a size, about: each sequence ends in a piece that is half full
-  auto pieces = [&](int tokens) { return p.Hkv * ((long long)p.T / tokens + nseq / 2); };
+  auto pieces = [&](int tokens) { return packed_pieces_estimate(p, tokens); };
   const int mean = p.T / nseq;
   const bool dense = p.L == 0 || dense_depth_supported(p);
   int tokens = full;

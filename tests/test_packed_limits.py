@@ -60,3 +60,27 @@ def test_good_bounds_with_as_many_sequences():
     r = joint_attention(q.double(), k[0].double(), v[0].double(), see, None, None, d ** -0.5)
     assert_close(out, r["out"], r["out_bound"], "out")
     assert_close(lse, r["lse"], LSE_BOUND, "lse")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [127, 128, 255, 257])
+@pytest.mark.parametrize("d,G,Hkv", [(128, 4, 64), (64, 2, 64), (64, 1, 75)])
+def test_one_sequence_about_a_block_long_with_many_heads(N, d, G, Hkv):
+    # around the counts of blocks at which CTAs share a walk, and tiles are cut smaller
+    g = torch.Generator(device="cuda").manual_seed(N + d)
+    q, dout = randn(g, G * Hkv, N, d), randn(g, G * Hkv, N, d)
+    k, v = randn(g, Hkv, N, d), randn(g, Hkv, N, d)
+    cu = torch.tensor([0, N], device="cuda", dtype=torch.int32)
+    out, lse = moda.forward_packed(q, k, v, cu)
+    grads = moda.backward_packed(q, k, v, cu, None, None, out, lse, dout)
+    moda.check_device_errors()
+    see = torch.ones(N, N, device="cuda", dtype=torch.bool).tril()
+    for h in range(0, Hkv, 7):
+        rows = slice(h * G, h * G + G)
+        r = joint_attention(q[rows].double(), k[h].double(), v[h].double(), see, None, None,
+                            d ** -0.5, dout[rows].double())
+        assert_close(out[rows], r["out"], r["out_bound"], f"out {h}")
+        assert_close(lse[rows], r["lse"], LSE_BOUND, f"lse {h}")
+        assert_close(grads["dq"][rows], r["dq"], r["dq_bound"], f"dq {h}")
+        assert_close(grads["dk"][h], r["dk"], r["dk_bound"], f"dk {h}")
+        assert_close(grads["dv"][h], r["dv"], r["dv_bound"], f"dv {h}")
