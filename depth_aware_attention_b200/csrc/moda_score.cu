@@ -199,7 +199,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (warp == 8 && lane < 2) tma_prefetch_desc(lane ? &tmQ : &tmK);
+  bool no_loads = false;
+  if (warp == 8) {
+    if (lane < 2) tma_prefetch_desc(lane ? &tmQ : &tmK);
+    // test-only fault: issue no loads, so that every wait for them runs out
+    no_loads = g_device_fault == kFaultForwardNoLoads;
+  }
   long long n = 0;
   for (int b = lane; b < a.B; b += 32) n += score_blocks(a, b);
 #pragma unroll
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA
-    if (lane == 0) {
+    if (lane == 0 && !no_loads) {
       int e = 0;
       ScoreWalk w = walk0;
       bool more = true;
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (*abort_flag)  // abort path: what was issued still lands; wait for it before exit
         for (int i = e > NS ? e - NS : 0; i < e; ++i)
           mbar_wait_drain(bar(bars->full[i % NS]), (i / NS) & 1);
-    } else if (lane == 1) {
+    } else if (lane == 1 && !no_loads) {
       ScoreWalk w = walk0;
       int pc = 0;
       bool more = true;

@@ -536,9 +536,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile int* abort_flag = &bars->abort;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 8 && lane < 7) {
-    const CUtensorMap* maps[7] = {&tmQ, &tmK, &tmV, &tmKT, &tmVT, &tmKD, &tmVD};
-    tma_prefetch_desc(maps[lane]);
+  bool no_loads = false;
+  if (warp == 8) {
+    if (lane < 7) {
+      const CUtensorMap* maps[7] = {&tmQ, &tmK, &tmV, &tmKT, &tmVT, &tmKD, &tmVD};
+      tma_prefetch_desc(maps[lane]);
+    }
+    // test-only fault: issue no loads, so that every wait for them runs out
+    no_loads = g_device_fault == kFaultForwardNoLoads;
   }
 
   // warp 0 finds this CTA's work (prompts: every warp an item) while others set up the barriers
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA
-    if (lane == 0) {
+    if (lane == 0 && !no_loads) {
       int e = 0;
       TreeWalk w = walk0;
       bool more = true;
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (*abort_flag)  // abort path: what was issued still lands; wait for it before exit
         for (int i = e > NS ? e - NS : 0; i < e; ++i)
           mbar_wait_drain(bar(bars->full[i % NS]), (i / NS) & 1);
-    } else if (lane == 1) {
+    } else if (lane == 1 && !no_loads) {
       TreeWalk w = walk0;
       int pc = 0;  // piece
       bool more = true;

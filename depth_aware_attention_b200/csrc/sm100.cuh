@@ -26,8 +26,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 // Test knobs, set only through moda_test_set_device_fault(): the limit every bounded wait
 // uses (kWaitLimitNs unless a test shortens it), and a fault the kernels inject on purpose
-// so that a test can watch the waits run out (0: none; kFaultForwardNoLoads: the forward
-// kernel's TMA producer issues no loads, so every wait for its data runs out).
+// so that a test can watch the waits run out (0: none; kFaultForwardNoLoads: the TMA producers of
+// the forward, the tree and the score kernels issue no loads, so every wait for their data runs
+// out).
 constexpr int kFaultForwardNoLoads = 1;
 __device__ uint64_t g_wait_limit_ns = kWaitLimitNs;
 __device__ int g_device_fault = 0;

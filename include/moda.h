@@ -384,11 +384,11 @@ moda_status_t moda_check_device_errors(moda_stream_t stream, uint32_t *flags);
  * calling thread's current device, the limit every bounded kernel wait uses and a fault
  * the kernels inject on purpose:
  *   fault 0  none (the normal state);
- *   fault 1  the forward kernel's TMA producer issues no loads, so every wait for that
- *            data runs out after wait_limit_ns: each CTA records the timeout in the
- *            device error word, lets the operations it has in flight finish, releases its
- *            tensor memory and exits (its out and lse are then meaningless), and
- *            moda_check_device_errors() returns MODA_ERR_TIMEOUT.
+ *   fault 1  the TMA producers of the forward, the tree attention and the score kernels
+ *            issue no loads, so every wait for that data runs out after wait_limit_ns: each
+ *            CTA records the timeout in the device error word, lets the operations it has in
+ *            flight finish, releases its tensor memory and exits (what it wrote is then
+ *            meaningless), and moda_check_device_errors() returns MODA_ERR_TIMEOUT.
  * wait_limit_ns: 0 restores the default limit (2 s), otherwise 1e5..1e10 ns.  Call it
  * with no kernel of this library in flight on the device, and call it again with (0, 0)
  * afterwards.  MODA_ERR_INVALID_ARGUMENT for other values, MODA_ERR_CUDA or
