@@ -66,7 +66,8 @@ __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int 
     else
       hi = mid;
   }
-  int rank = int(uint32_t(c) - total(lo + 1));
+  // (below zero only where the counts have wrapped: then some lane still holds it)
+  int rank = max(0, int(uint32_t(c) - total(lo + 1)));
   for (int s0 = 0; s0 < nseq; s0 += 32) {
     const int s = s0 + lane;
     const int n = s0 == 0 ? n0 : (s < nseq ? pieces(s) : 0);
@@ -75,9 +76,7 @@ __device__ __forceinline__ PackedPiece packed_find(const int* cu, int nseq, int 
     if (rank < here) {
       // the lane that holds the rank-th of these sequences
       const bool mine = n > lo && __popc(m & ((1u << lane) - 1u)) == rank;
-      const uint32_t holder = __ballot_sync(0xffffffffu, mine);
-      if (holder == 0u) return r;  // (a rank below zero, after a wrap)
-      const int src = __ffs(holder) - 1;
+      const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
       const int len = mine ? packed_len(cu, s, N, first, bad) : 0;
       r.first = __shfl_sync(0xffffffffu, first, src);
       r.len = __shfl_sync(0xffffffffu, len, src);
