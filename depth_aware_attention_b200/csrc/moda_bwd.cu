@@ -961,7 +961,8 @@ __device__ __forceinline__ void own_tile_rows(const SeqArgs& a, const SeqSpan& w
 // Packed batches are short walks, where the time of one tile counts: there the P/dS work of a
 // tile is shared by two groups of four warps (0-3 rows [0, 64), 12-15 rows [64, 128)), and dQ
 // has TMEM columns and a staging buffer of its own, so that the next tile's S^T and dP^T need
-// not wait for its readout.  (11 sequences of 2003 tokens, 6 heads: 61 us with the other order.)
+// not wait for its readout.  (2003 tokens in 11 sequences, 6 heads, this kernel without shared walks:
+// 48 us, 61 with the other order.)
 constexpr int kSeqPackedThreads = 512;
 template <int D, bool kPacked>
 __global__ void __launch_bounds__(kPacked ? kSeqPackedThreads : kSeqThreads, 1)
@@ -2064,10 +2065,13 @@ inline BwdLayout bwd_layout(const Problem& p) {
 
 // CTAs that share the walk of one key block of a packed batch: as many as fill the GPU while
 // the blocks are few; two also for up to two waves of blocks whose walks are long, which then
-// end more evenly.  Each CTA more costs about as much as two tiles.  (Forward and backward, 16
-// heads in groups of 4, d = 128: 600 tokens, 24 blocks, 82 / 66 / 59 us with 1 / 2 / 4 CTAs; 3000
-// in 20 sequences, 133 blocks, 197 / 158 / 207; 6000 in 10, 207 blocks of about 9 tiles, 367 /
-// 311 / 392; 8000 in 60, 370 blocks of 2 tiles, 316 / 352 / 500.)
+// end more evenly.  Each CTA more costs about as much as two tiles.  (Forward and backward from a
+// graph, 16 heads in groups of 4, d = 128, L = 24, log-normal lengths: 600 tokens in 3 sequences, 24
+// blocks, 98 / 89 / 84 us with 1 / 2 / 4 CTAs; 3000 in 20, 133 blocks, 244 / 215 / 260; 6000 in 10,
+// 207 blocks of about 9 tiles, 484 / 410 / 490; 8000 in 60, 370 blocks of 2 tiles, 458 / 506 / 650;
+// 16384 in 24, 560 blocks, 1145 / 1215 / 1482.)  The mean is all that the host knows: the walks of one
+// long sequence among short ones, or among empty slots, are not shared (2000 tokens in one sequence,
+// backward 166 us, and 284 with 511 empty slots behind it).
 int walk_ctas(const Problem& p) {
   const int nseq = p.nseq < p.T ? p.nseq : p.T;
   const long long blocks = packed_pieces_estimate(p, 128);

@@ -6,7 +6,8 @@
 // old order, and their old positions written down.
 //
 // What bounds it: the copy of the kept rows (HBM), once the selection is quick (16 rows of 64K
-// scores, 8192 kept, d = 128: selection 18.5 us, copy 21 us for 134 MB).  Two launches:
+// scores, 8192 kept, d = 128: 41.6 us from a graph; in the profiler the selection takes 20 and the copy
+// 21 for 134 MB).  Two launches:
 //   1. moda_evict_select_kernel: a radix selection.  A float's bits map to an integer of the
 //      same order; protected entries get the largest integer, so that one selection of the
 //      `keep` largest finds the whole set.  Four passes of 8 bits, from the top, each count the

@@ -10,8 +10,9 @@
 //
 // What bounds it: each key is read once and meets the G x N rows of its KV head.  Up to about
 // 128 rows that is a stream of K from HBM; beyond, the exponentials take longer.  (8 caches of up
-// to 64K keys, 16 heads, one token: 65 us, 5.7 TB/s; 33 tokens over 2 caches of 5000, d = 64:
-// 12 us, a CTA's own latency.)
+// to 64K keys, 16 heads, one token, from a graph: 68 us, 5.5 TB/s; 33 tokens over 2 caches of 5000,
+// d = 64: 14.3 us, a CTA's own latency.  More than three row tiles read K again in another launch: the
+// same 8 caches, 96 tokens 237 us, 128 tokens 334.)
 //   The products are S^T = K Q^T: a key is a TMEM lane, so one thread owns one key and adds its
 // weights up in a register, in a fixed order -- no reduction across threads, no atomics, the
 // same bits every run.  The row tiles (up to three of 128 rows; more rows take more launches)

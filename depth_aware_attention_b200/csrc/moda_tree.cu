@@ -7,9 +7,10 @@
 // itself, and its own L depth entries, in one joint softmax.  N = 1 is single-token decoding
 // over caches of different lengths.  (The pages describe neither.)
 //
-// What bounds it (one B200): 32 caches of 10K-32K keys, one token each, 220 us sustained, 6.7
-// TB/s; 61 drafts over 2 caches of up to 64K, 32 heads, 125 us in a graph, 0.77 PFLOP/s and 3.3
-// TB/s; 4 caches of 1000, one token, 11 us in a graph, two launches' latency.
+// What bounds it (one B200, both launches, from a graph): 32 caches of 10K-32K keys, one token each,
+// 16 heads in groups of 4, L = 48: 216 to 223 us, 6.6 TB/s; 61 drafts over 2 caches of up to 64K,
+// 32 heads, L = 32: 140 to 147 us, 0.7 PFLOP/s and 2.9 TB/s, 11 of them the joining; 4 caches of
+// 1000, one token, L = 24: 12.3 us, two launches' latency.
 // Each cached K/V byte is needed once and serves the G x N rows of its KV
 // head, so up to 128 rows the work is a stream from HBM and the tensor cores have the FLOPs
 // to spare; from 128 to 256 rows both take about as long.
@@ -31,9 +32,8 @@
 //   Few rows (template flag kThin: up to 16 rows, d = 128).  One token of a group of 4 fills 4 of
 //   the 128 rows, and the idle rest costs power and with it the clock, and the softmax's time.
 //   Here the products are transposed, S^T = K Q^T and O^T = V^T P^T, with 16 columns for the
-//   rows: an eighth of the products, and a thread holds one key instead of one row.  (32 caches
-//   of 10K-32K keys, one token: 247 -> 220 us sustained; 4 caches of 1000: 14.0 -> 11.0 in a
-//   graph.)
+//   rows: an eighth of the products, and a thread holds one key instead of one row.  (Both sides'
+//   times are at launch_tree.)
 //   Prompts (template flag kPrompt).  The same machinery computes the packed forward of small
 //   batches and of groups the forward kernel has no dense depth path for: an item is a tile (or
 //   pair) of one sequence's tokens, its steps are the depth entries and the key blocks up to its
@@ -340,6 +340,7 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t n, bool p) {
 // an eighth of the full tile's.  Each row keeps a reference m that all threads of the warpgroup
 // share; it moves only when a score exceeds it by 2^kTreeRescale, which one barrier with an OR
 // finds out, and l is summed per thread until the piece's end.
+// P is rounded to bf16 as in the full form.
 //   scratch: [2 warpgroups][4 warps][16] partial results, [2][16] (m, l), [2][16] ancestor bits
 template <int D, int kRows>
 __device__ __forceinline__ void thin_softmax(const TreeArgs& a, TreeBars* bars,
@@ -887,7 +888,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
     };
-    // P enters its product as bf16 (the products' operand type); l sums it unrounded.
+    // P enters its product as bf16 (the products' operand type); l sums it unrounded.  Each
+    // weight is then off by at most 2^-8 of itself, independently: over the measured cases out
+    // differs from 64 bits by 2.1e-3 to 2.4e-3 of its size, where rounding out alone gives 1.7e-3.
+    // A second product with what the rounding left would bring that back, for twice the work with V.
     // All 128 keys of a step.  Without a mask (a block inside the cache) every fourth pair of
     // exponentials is computed on the FMA pipe, as in the forward.
     auto full_step = [&](auto masked_c, const uint32_t (&vis)[4]) {
@@ -1396,9 +1400,10 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
   using D128 = std::integral_constant<int, 128>;
   using D64 = std::integral_constant<int, 64>;
   // Few rows: the transposed products, with 4 rows' exponentials a thread or with 16.  (d = 64 has
-  // no such form: its O^T would have 64 lanes.)  In a graph, 4-row form / 16-row form / full tiles:
-  // 4 rows, 4 caches of 1000 keys 12.7 / 15.7 / 15.7 us, 32 of 10K-32K 216 / 221 / 230; 16 rows
-  // (4 tokens), - / 16.1 / 15.7 and - / 228 / 237.
+  // no such form: its O^T would have 64 lanes.)  From a graph, 16 heads in groups of 4, 4-row form /
+  // 16-row form / full tiles: one token (4 rows), 4 caches of 1000 keys with L = 24: 12.3 / 16.2 /
+  // 15.9 us, 32 of 10K-32K with L = 48: 223 / 229 / 235; 4 tokens (16 rows), - / 16.4 / 16.4 and
+  // - / 235 / 247.
   const int rows = p.N * (p.Hq / p.Hkv);
   if (p.d == 128 && rows <= 4)
     return launch_tree_d<128, false, false, 4>(p, t, a, q, k, v, kt, vt, kd, vd, encode, stream,
@@ -1416,15 +1421,19 @@ cudaError_t launch_tree(const TreeProblem& p, const void* q, const void* k, cons
 // tile with the loads already under way.  So single tiles are taken
 //   - while their CTAs fit the GPU at once, smaller ones as long as that still holds: with few
 //     tokens a tile, a depth step holds more of each token's entries (16 heads in groups of 4,
-//     d = 128, L = 24: 411 tokens in 5 sequences 13 us against the forward kernel's 21);
+//     d = 128, L = 24: 411 tokens in 5 sequences 14.4 us, 17.4 in full tiles, against the forward
+//     kernel's 22.5);
 //   - for short sequences, about as long as a tile or shorter, in tiles of up to twice their
-//     length (1500 tokens in 181: 62 us against 103; 4000 in 200: 99 against 134; 4000 in 64, mean
-//     62: 84 against 77, so not there);
+//     length (1500 tokens in 181: 60 us against 105; 4000 in 200: 99 against 135; 4000 in 64, mean
+//     62: 85 against 79, so not there);
 //   - for sequences of up to five tiles when each CTA gets several (12000 tokens in 200, d = 64,
-//     L = 8: 93 us against 124; 16000 in 50, L = 0, mean 320: 145 against 134, so not there).
+//     L = 8: 94 us against 126; 16000 in 50, L = 0, mean 320: 136 against 123, so not there).
 // Groups without a dense depth path in the forward kernel run here at any size: in pairs of
 // tiles once single ones no longer fit and sequences are long (groups of 3, d = 64, L = 7: 5000
-// tokens in 37 sequences 26 us in single tiles and 31 in pairs; 9000 in 30, 50 and 41).
+// tokens in 37 sequences 26 us in single tiles and 33 in pairs; 9000 in 30, 42 and 41).
+// (From a graph; log-normal lengths, sigma 1.)  The mean is all that the host knows: where one
+// sequence is much longer than the others, or slots of cu_seqlens are empty, the variant may be the
+// slower one (one sequence of 64K tokens 15.3 ms, and 19.9 with 1023 empty slots behind it).
 PromptTile prompt_tile(const Problem& p) {
   const int full = 128 / p.G;
   const int nseq = p.nseq < p.T ? p.nseq : p.T;
